@@ -376,6 +376,139 @@ int moe_decode_layer_noalloc(const uint16_t* x, int M, int H,
                              int32_t* status, void* stream);
 
 /* ------------------------------------------------------------------------- */
+/* MXFP4: 4-bit floating point with a power-of-two scale per 32 values ([CMP]: */
+/* routed experts held at 4 bits; the matrix cores take this format as it is). */
+/* ------------------------------------------------------------------------- */
+
+/* MXFP4 quantisation of `rows` rows of K values.  A block is 32 consecutive
+ * values of a row; its scale byte b stands for 2^(b - 127):
+ *   b = max(floor(log2(amax)) - 2 + 127, 0);  127 if amax = 0;  255 (NaN, with
+ *   every code 0) if a value of the block is infinite or NaN.
+ * A value's code is the E2M1 level (0 .5 1 1.5 2 3 4 6, bit 3 the sign) nearest
+ * to v / 2^(b - 127), ties to the even code, magnitudes above 6 to 6.
+ *   in      : bf16 [rows,K] if in_is_f32 == 0, fp32 [rows,K] otherwise
+ *   codes   : uint8 [rows,K/2] (output), low nibble = even k
+ *   scales  : uint8 [rows,K/32] (output)
+ * Constraints: rows >= 1, K >= 32, K % 32 == 0. */
+int pq_quantize_mxfp4(const void* in, int in_is_f32, int rows, int K,
+                      uint8_t* codes, uint8_t* scales, void* stream);
+
+/* The values of codes and scale bytes: bf16 [rows,K] if out_is_f32 == 0, fp32
+ * otherwise.  Exact, but for blocks with the scale bytes 253 and 254, whose
+ * largest values pass the type's range and come out infinite (pq_quantize_mxfp4
+ * makes none above 252); a block with the byte 255 comes out as NaN. */
+int pq_dequantize_mxfp4(const uint8_t* codes, const uint8_t* scales, int rows, int K,
+                        int out_is_f32, void* out, void* stream);
+
+/* y = epi(bf16( sum_k x[m,k] w[n,k] )), w the values of (codes, scale bytes), x
+ * as it is, fp32 accumulation: the weight-streaming form for few tokens.
+ *   x : bf16 [M,K]    w : codes [N,K/2]    w_scale : bytes [N,K/32]
+ *   y : bf16 [M,N] or [M,N/2] under PQ_EPI_SILU_MUL (gate rows then up rows)
+ * Constraints: 1 <= M <= 16, K % 32 == 0, K >= 32, N >= 1, N even under
+ * PQ_EPI_SILU_MUL, N*K/2 < 2^31, M*K <= 69632 (the activation lives in one
+ * CU's LDS); PQ_ERR_SHAPE otherwise.  An output's bits depend on K, N, the
+ * epilogue and the device's CU count, not on M or the other tokens, as long as
+ * N is below 2048 rows per CU.  No workspace. */
+int pq_gemv_mxfp4(const uint16_t* x, int M, int K,
+                  const uint8_t* w, const uint8_t* w_scale, int N,
+                  int epi, uint16_t* y, void* stream);
+
+/* Workspace bytes of pq_gemm_mxfp4: the data-region offset of the shared
+ * workspace layout plus the quantised activation; 0 for invalid shapes. */
+size_t pq_gemm_mxfp4_workspace(int M, int K, int N, int epi);
+
+/* y = epi(bf16( q(x) w^T )) for any M >= 1 on the matrix cores, q(x) the values
+ * of the live MXFP4 quantisation of x (the rule of pq_quantize_mxfp4): two
+ * launches on `stream`.  Operands and epilogue as pq_gemv_mxfp4.
+ *   ws, ws_bytes : workspace of pq_gemm_mxfp4_workspace() bytes.  Only its data
+ *       region is used, as scratch, so it needs no pq_workspace_init and may be
+ *       the workspace of the other entry points; calls that share it must be
+ *       ordered (one stream).
+ * Constraints: K % 32 == 0, N >= 1, N*K/2 < 2^31, M*K/2 < 2^31, N even under
+ * PQ_EPI_SILU_MUL.  An output's bits do not depend on the other tokens. */
+int pq_gemm_mxfp4(const uint16_t* x, int M, int K,
+                  const uint8_t* w, const uint8_t* w_scale, int N,
+                  int epi, uint16_t* y, void* ws, size_t ws_bytes, void* stream);
+
+/* The product alone, on an activation that pq_quantize_mxfp4 made:
+ *   xq : codes [M,K/2]    xs : bytes [M,K/32].  One launch, no workspace. */
+int pq_gemm_mxfp4_prequant(const uint8_t* xq, const uint8_t* xs, int M, int K,
+                           const uint8_t* w, const uint8_t* w_scale, int N,
+                           int epi, uint16_t* y, void* stream);
+
+/* ------------------------------------------------------------------------- */
+/* Routed rows in expert order: the steps of an MoE layer for a prompt's or a   */
+/* training step's tokens.  A pair p = m * top_k + s is slot s of token m; P =  */
+/* M * top_k pairs.                                                            */
+/* ------------------------------------------------------------------------- */
+
+/* Workspace bytes of pq_moe_sort (0 where one block sorts the batch). */
+size_t pq_moe_sort_workspace(int M, int top_k, int E);
+
+/* Sort the pairs by expert, pairs of one expert in pair order.
+ *   topk_ids : int32 [M,top_k]; an id outside [0,E) stands for no expert (a
+ *              padded token, or an expert of another device)
+ *   order    : int32 [P] (output): the pair at sorted row r; -1 from row
+ *              offsets[E] on
+ *   inverse  : int32 [M,top_k] (output): the pair's row; -1 for no expert
+ *   offsets  : int32 [E+1] (output): expert e has rows offsets[e] ..
+ *              offsets[e+1] - 1
+ *   ws       : workspace of pq_moe_sort_workspace() bytes, scratch as in
+ *              pq_gemm_mxfp4
+ * Constraints: M, top_k >= 1, 1 <= E <= 1024, M * top_k < 2^31.  One launch, two
+ * where there are more than 2048 pairs. */
+int pq_moe_sort(const int32_t* topk_ids, int M, int top_k, int E,
+                int32_t* order, int32_t* inverse, int32_t* offsets,
+                void* ws, size_t ws_bytes, void* stream);
+
+/* xs[r] = x[order[r] / top_k]; zeros in the rows without a pair.
+ *   x : bf16 or fp32 [M,H]    xs : the same type, [P,H]    (order, inverse): of
+ *   pq_moe_sort.  H % 8 == 0.  xs must not overlap x. */
+int pq_moe_dispatch(const void* x, int is_f32, int M, int H, int top_k,
+                    const int32_t* order, const int32_t* inverse, void* xs, void* stream);
+
+/* y[m] = sum_s topk_w[m,s] ys[inverse[m,s]], added in fp32 in slot order,
+ * slots without an expert left out (a token without any gets zeros).
+ *   ys : bf16 or fp32 [P,H]    topk_w : fp32 [M,top_k]    y : like ys, [M,H]
+ * With topk_w NULL every weight is 1, which makes the call the gradient of
+ * pq_moe_dispatch: dx[m] = sum_s dxs[inverse[m,s]].  y must not overlap ys. */
+int pq_moe_combine(const void* ys, int is_f32, int M, int H, int top_k,
+                   const int32_t* inverse, const float* topk_w, void* y, void* stream);
+
+/* The gradients of pq_moe_combine for dy [M,H], with p the pair of row r:
+ *   dys[r] = topk_w[p] dy[p / top_k], zeros in the rows without a pair
+ *   dw[p]  = sum_h dy[p / top_k, h] ys[r, h] in fp32, 0 for a pair without one
+ *   dys : like ys, [P,H]    dw : fp32 [M,top_k] */
+int pq_moe_combine_grad(const void* dy, const void* ys, int is_f32, int M, int H, int top_k,
+                        const int32_t* order, const int32_t* inverse, const float* topk_w,
+                        void* dys, float* dw, void* stream);
+
+/* Workspace bytes of pq_gemm_mxfp4_grouped for `rows` rows of x. */
+size_t pq_gemm_mxfp4_grouped_workspace(int rows, int K, int N, int epi);
+
+/* The experts' products over rows in expert order: for e and r in
+ * offsets[e] .. offsets[e+1] - 1
+ *   y[r] = epi(bf16( q(x[src(r)]) w_e^T )),  zeros in the rows from offsets[E] on
+ * with src(r) = order[r] / top_k where order is given (x holds the tokens, read
+ * in place: no sorted copy), else r (x holds the sorted rows).
+ *   x : bf16 [rows,K], rows = P / top_k with order, P without
+ *   w : codes [E,N,K/2]    w_scale : bytes [E,N,K/32]    y : bf16 [P,R], R = N,
+ *       or N/2 under PQ_EPI_SILU_MUL
+ *   (order, offsets) : of pq_moe_sort; ws as in pq_gemm_mxfp4
+ * Constraints as pq_gemm_mxfp4 (one expert's N*K/2 < 2^31), 1 <= E <= 1024.  Two
+ * launches. */
+int pq_gemm_mxfp4_grouped(const uint16_t* x, int rows, int K,
+                          const int32_t* order, int top_k, const int32_t* offsets, int P, int E,
+                          const uint8_t* w, const uint8_t* w_scale, int N,
+                          int epi, uint16_t* y, void* ws, size_t ws_bytes, void* stream);
+
+/* The products alone, on rows that pq_quantize_mxfp4 made.  One launch. */
+int pq_gemm_mxfp4_grouped_prequant(const uint8_t* xq, const uint8_t* xs, int rows, int K,
+                                   const int32_t* order, int top_k, const int32_t* offsets, int P, int E,
+                                   const uint8_t* w, const uint8_t* w_scale, int N,
+                                   int epi, uint16_t* y, void* stream);
+
+/* ------------------------------------------------------------------------- */
 /* Workspace and error helpers.                                               */
 /* ------------------------------------------------------------------------- */
 
@@ -392,10 +525,12 @@ const char* pq_strerror(int status);
 /* HIP error code of the last PQ_ERR_HIP returned on the calling thread. */
 int pq_last_hip_error(void);
 
-/* Kernel launches one call of the named entry point makes ("pq_gemm_fp8": 2,
- * the activation quantisation and the GEMM; every other compute entry point:
- * 1, including the whole MoE layer; moe_decode_layer_noalloc adds one
- * zeroing launch on the first call on each device).  PQ_ERR_NULL for NULL,
+/* Kernel launches one call of the named entry point makes ("pq_gemm_fp8",
+ * "pq_gemm_mxfp4" and "pq_gemm_mxfp4_grouped": 2, the activation quantisation
+ * and the GEMM; "pq_moe_sort": 2, one of them left out for at most 2048 pairs;
+ * every other compute entry point: 1, including the whole MoE layer;
+ * moe_decode_layer_noalloc adds one zeroing launch on the first call on each
+ * device).  PQ_ERR_NULL for NULL,
  * PQ_ERR_UNSUPPORTED for a name that is not a compute entry point. */
 int pq_launches_per_call(const char* entry_point);
 

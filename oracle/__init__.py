@@ -39,11 +39,14 @@ from .codecs import (E4M3_MAX, e4m3_decode, e4m3_encode, bf16_round, bf16_bits,
 from .quant import block_quant_fp8, act_quant_fp8, dequant_fp8, q4_quant, dequant_q4
 from .linear import gemv_fp8, silu_mul, gemv_q4
 from .moe import route_topk, router_logits, moe_layer, union_of_experts
+from .mxfp4 import (E2M1, mx_quant, mx_scale, mx_values, mx_product, route_sort, route_dispatch,
+                    route_combine, route_combine_grad)
 from . import traffic
 
 __all__ = [
     "E4M3_MAX", "e4m3_decode", "e4m3_encode", "bf16_round", "bf16_bits", "bf16_bits_to_f64",
     "q4_pack", "q4_unpack", "block_quant_fp8", "act_quant_fp8", "dequant_fp8", "q4_quant",
     "dequant_q4", "gemv_fp8", "silu_mul", "gemv_q4", "route_topk", "moe_layer",
-    "union_of_experts", "traffic",
+    "union_of_experts", "traffic", "E2M1", "mx_quant", "mx_scale", "mx_values", "mx_product", "route_sort",
+    "route_dispatch", "route_combine", "route_combine_grad",
 ]

@@ -9,6 +9,7 @@ CPU fallback: the library must be built (see ``build.py``).
 from __future__ import annotations
 
 import ctypes
+from typing import NamedTuple
 
 import torch
 
@@ -18,6 +19,9 @@ __all__ = ["PqError", "quantize_fp8", "quantize_q4", "gemv_fp8", "gemm_fp8", "ge
            "gemv_q4_group", "moe_decode_layer",
            "moe_decode_layer_noalloc", "gemv_fp8_workspace_bytes", "moe_workspace_bytes", "workspace_check",
            "launches_per_call", "moe_layer_config",
+           "quantize_mxfp4", "dequantize_mxfp4", "gemv_mxfp4", "gemm_mxfp4", "gemm_mxfp4_prequant",
+           "MoePlan", "moe_sort", "moe_dispatch", "moe_dispatch_grad", "moe_combine", "moe_combine_grad",
+           "gemm_mxfp4_grouped", "gemm_mxfp4_grouped_prequant", "moe_prefill_layer_mxfp4",
            "stream_probe",
            "EPI_NONE", "EPI_SILU_MUL", "lib"]
 
@@ -403,3 +407,265 @@ class MoeLayerCall:
 
     def check(self) -> int:
         return lib().pq_workspace_check(_p(self.ws), _stream())
+
+
+# ---------------------------------------------------------------------------
+# MXFP4, and routed rows in expert order.  These calls take their scratch from
+# torch's allocator per call, on the current stream, so calls on several
+# streams and captured graphs never share it.
+# ---------------------------------------------------------------------------
+
+def _need_here(t, dtypes, ndim, name):
+    """_need for one of several dtypes, and on the current device, whose stream the call goes to."""
+    if isinstance(t, torch.Tensor) and t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    _need(t, t.dtype if isinstance(t, torch.Tensor) else None, ndim, name)
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _out(out, shape, dtype, like, name="out"):
+    """The given output, checked, or a new one."""
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    _need_here(out, (dtype,), len(shape), name)
+    if tuple(out.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(out.shape)}")
+    return out
+
+
+def _apart(out, out_name, **inputs):
+    """An output that a kernel writes while others of its blocks still read the inputs must not overlap them."""
+    b, e = out.data_ptr(), out.data_ptr() + out.numel() * out.element_size()
+    for name, t in inputs.items():
+        if t is not None and t.data_ptr() < e and b < t.data_ptr() + t.numel() * t.element_size():
+            raise ValueError(f"{out_name} must not overlap {name}")
+
+
+_ROW_TYPES = (torch.bfloat16, torch.float32)
+
+
+def quantize_mxfp4(t: torch.Tensor):
+    """MXFP4 quantisation of bf16 or fp32 rows [R, K] -> (codes uint8 [R, K/2], scale bytes uint8 [R, K/32])."""
+    _need_here(t, _ROW_TYPES, 2, "t")
+    R, K = t.shape
+    codes = torch.empty((R, K // 2), dtype=torch.uint8, device=t.device)
+    scales = torch.empty((R, max(K // 32, 1)), dtype=torch.uint8, device=t.device)
+    _check(lib().pq_quantize_mxfp4(_p(t), int(t.dtype == torch.float32), R, K, _p(codes), _p(scales), _stream()),
+           "pq_quantize_mxfp4")
+    return codes, scales
+
+
+def dequantize_mxfp4(codes, scales, dtype=torch.bfloat16, out=None):
+    """The values [R, K] (bf16 or fp32) of MXFP4 codes uint8 [R, K/2] and scale bytes uint8 [R, K/32]."""
+    _need_here(codes, (torch.uint8,), 2, "codes")
+    _need_here(scales, (torch.uint8,), 2, "scales")
+    if dtype not in _ROW_TYPES:
+        raise TypeError("dequantize_mxfp4 gives bf16 or fp32")
+    R, K = codes.shape[0], codes.shape[1] * 2
+    if tuple(scales.shape) != (R, K // 32):
+        raise ValueError("code / scale shapes do not match")
+    y = _out(out, (R, K), dtype, codes)
+    _check(lib().pq_dequantize_mxfp4(_p(codes), _p(scales), R, K, int(dtype == torch.float32), _p(y), _stream()),
+           "pq_dequantize_mxfp4")
+    return y
+
+
+def _mx_weights(w, w_scale, K, ndim):
+    _need_here(w, (torch.uint8,), ndim, "w")
+    _need_here(w_scale, (torch.uint8,), ndim, "w_scale")
+    if w.shape[-1] * 2 != K or w_scale.shape[:-1] != w.shape[:-1] or w_scale.shape[-1] * 32 != K:
+        raise ValueError("weight / scale shapes do not match x")
+    return w.shape[-2]
+
+
+def gemv_mxfp4(x, w, w_scale, epi: int = EPI_NONE, out=None):
+    """y = epi(x @ w^T) for few tokens: x bf16 [M,K] as it is, M <= 16, w MXFP4 codes [N,K/2] and scale bytes
+    [N,K/32].  Returns y (bf16 [M,N] or [M,N/2])."""
+    _need_here(x, (torch.bfloat16,), 2, "x")
+    M, K = x.shape
+    N = _mx_weights(w, w_scale, K, 2)
+    y = _out(out, (M, N // 2 if epi == EPI_SILU_MUL else N), torch.bfloat16, x)
+    _apart(y, "out", x=x, w=w, w_scale=w_scale)
+    _check(lib().pq_gemv_mxfp4(_p(x), M, K, _p(w), _p(w_scale), N, epi, _p(y), _stream()), "pq_gemv_mxfp4")
+    return y
+
+
+def gemm_mxfp4(x, w, w_scale, epi: int = EPI_NONE, out=None):
+    """y = epi(q(x) @ w^T) on the matrix cores: x bf16 [M,K], quantised live to MXFP4, w codes [N,K/2] and scale
+    bytes [N,K/32].  Returns y (bf16 [M,N] or [M,N/2])."""
+    _need_here(x, (torch.bfloat16,), 2, "x")
+    M, K = x.shape
+    N = _mx_weights(w, w_scale, K, 2)
+    y = _out(out, (M, N // 2 if epi == EPI_SILU_MUL else N), torch.bfloat16, x)
+    _apart(y, "out", w=w, w_scale=w_scale)
+    wsn = int(lib().pq_gemm_mxfp4_workspace(M, K, N, epi))
+    ws = torch.empty(wsn, dtype=torch.uint8, device=x.device)
+    _check(lib().pq_gemm_mxfp4(_p(x), M, K, _p(w), _p(w_scale), N, epi, _p(y), _p(ws), wsn, _stream()),
+           "pq_gemm_mxfp4")
+    return y
+
+
+def _mx_rows(xq, xs):
+    _need_here(xq, (torch.uint8,), 2, "xq")
+    _need_here(xs, (torch.uint8,), 2, "xs")
+    rows, K = xq.shape[0], xq.shape[1] * 2
+    if tuple(xs.shape) != (rows, K // 32):
+        raise ValueError("xq / xs shapes do not match")
+    return rows, K
+
+
+def gemm_mxfp4_prequant(xq, xs, w, w_scale, epi: int = EPI_NONE, out=None):
+    """The GEMM of gemm_mxfp4 on an activation that quantize_mxfp4 made (xq [M,K/2], xs [M,K/32])."""
+    M, K = _mx_rows(xq, xs)
+    N = _mx_weights(w, w_scale, K, 2)
+    y = _out(out, (M, N // 2 if epi == EPI_SILU_MUL else N), torch.bfloat16, xq)
+    _apart(y, "out", xq=xq, xs=xs, w=w, w_scale=w_scale)
+    _check(lib().pq_gemm_mxfp4_prequant(_p(xq), _p(xs), M, K, _p(w), _p(w_scale), N, epi, _p(y), _stream()),
+           "pq_gemm_mxfp4_prequant")
+    return y
+
+
+class MoePlan(NamedTuple):
+    """Routed (token, slot) pairs in expert order, as moe_sort makes it (int32 device tensors)."""
+    order: torch.Tensor     # [P] the pair m * top_k + s at each sorted row, -1 behind the last
+    inverse: torch.Tensor   # [M, top_k] the sorted row of each pair, -1 for a pair without an expert
+    offsets: torch.Tensor   # [E + 1] first sorted row of each expert
+
+
+def _plan(plan, need_offsets=False):
+    _need_here(plan.inverse, (torch.int32,), 2, "plan.inverse")
+    _need_here(plan.order, (torch.int32,), 1, "plan.order")
+    M, k = plan.inverse.shape
+    if plan.order.shape[0] != M * k:
+        raise ValueError("plan.order must have one entry per pair of plan.inverse")
+    if need_offsets:
+        _need_here(plan.offsets, (torch.int32,), 1, "plan.offsets")
+    return M, k
+
+
+def moe_sort(topk_ids, E: int) -> MoePlan:
+    """Sort the (token, slot) pairs of topk_ids int32 [M, top_k] by expert, pairs of one expert in pair order.
+    An id outside [0, E) stands for no expert (a padded token)."""
+    _need_here(topk_ids, (torch.int32,), 2, "topk_ids")
+    M, k = topk_ids.shape
+    dev = topk_ids.device
+    plan = MoePlan(torch.empty(M * k, dtype=torch.int32, device=dev),
+                   torch.empty((M, k), dtype=torch.int32, device=dev),
+                   torch.empty(max(int(E), 0) + 1, dtype=torch.int32, device=dev))
+    wsn = int(lib().pq_moe_sort_workspace(M, k, E))
+    ws = torch.empty(wsn, dtype=torch.uint8, device=dev) if wsn else None
+    _check(lib().pq_moe_sort(_p(topk_ids), M, k, E, _p(plan.order), _p(plan.inverse), _p(plan.offsets), _p(ws), wsn,
+                             _stream()), "pq_moe_sort")
+    return plan
+
+
+def moe_dispatch(x, plan: MoePlan, out=None):
+    """The tokens' rows in expert order: xs[r] = x[plan.order[r] // top_k], x bf16 or fp32 [M,H], xs [P,H]; the rows
+    without a pair are zeros."""
+    _need_here(x, _ROW_TYPES, 2, "x")
+    M, k = _plan(plan)
+    if x.shape[0] != M:
+        raise ValueError("x must have one row per token of the plan")
+    xs = _out(out, (M * k, x.shape[1]), x.dtype, x)
+    _apart(xs, "out", x=x)
+    _check(lib().pq_moe_dispatch(_p(x), int(x.dtype == torch.float32), M, x.shape[1], k, _p(plan.order),
+                                 _p(plan.inverse), _p(xs), _stream()), "pq_moe_dispatch")
+    return xs
+
+
+def moe_combine(ys, plan: MoePlan, topk_w=None, out=None):
+    """The experts' rows back at their tokens: y[m] = sum_s topk_w[m,s] ys[plan.inverse[m,s]] in fp32, ys bf16 or
+    fp32 [P,H], topk_w fp32 [M,top_k] (None: every weight 1).  A token without an expert gets zeros."""
+    _need_here(ys, _ROW_TYPES, 2, "ys")
+    M, k = _plan(plan)
+    if ys.shape[0] != M * k:
+        raise ValueError("ys must have one row per pair of the plan")
+    if topk_w is not None:
+        _need_here(topk_w, (torch.float32,), 2, "topk_w")
+        if topk_w.shape != plan.inverse.shape:
+            raise ValueError("topk_w must have the plan's shape [M, top_k]")
+    y = _out(out, (M, ys.shape[1]), ys.dtype, ys)
+    _apart(y, "out", ys=ys)
+    _check(lib().pq_moe_combine(_p(ys), int(ys.dtype == torch.float32), M, ys.shape[1], k, _p(plan.inverse),
+                                _p(topk_w), _p(y), _stream()), "pq_moe_combine")
+    return y
+
+
+def moe_dispatch_grad(dxs, plan: MoePlan, out=None):
+    """The gradient of moe_dispatch: dx[m] = sum_s dxs[plan.inverse[m,s]], added in fp32."""
+    return moe_combine(dxs, plan, None, out)
+
+
+def moe_combine_grad(dy, ys, plan: MoePlan, topk_w, out=None):
+    """The gradients of moe_combine for dy [M,H]: (dys [P,H] like ys, zeros in the rows without a pair; dw fp32
+    [M,top_k], 0 for a pair without an expert)."""
+    _need_here(dy, _ROW_TYPES, 2, "dy")
+    _need_here(ys, (dy.dtype,), 2, "ys")
+    _need_here(topk_w, (torch.float32,), 2, "topk_w")
+    M, k = _plan(plan)
+    H = dy.shape[1]
+    if dy.shape[0] != M or tuple(ys.shape) != (M * k, H) or topk_w.shape != plan.inverse.shape:
+        raise ValueError("dy, ys and topk_w must have the plan's tokens and pairs")
+    dys = _out(out, (M * k, H), ys.dtype, ys)
+    _apart(dys, "out", dy=dy, ys=ys)
+    dw = torch.empty((M, k), dtype=torch.float32, device=dy.device)
+    _check(lib().pq_moe_combine_grad(_p(dy), _p(ys), int(dy.dtype == torch.float32), M, H, k, _p(plan.order),
+                                     _p(plan.inverse), _p(topk_w), _p(dys), _p(dw), _stream()), "pq_moe_combine_grad")
+    return dys, dw
+
+
+def _grouped_args(rows, K, w, w_scale, plan, gather):
+    N = _mx_weights(w, w_scale, K, 3)
+    M, k = _plan(plan, True)
+    E = w.shape[0]
+    if plan.offsets.shape[0] != E + 1:
+        raise ValueError("plan.offsets must have one entry per expert of w, and one more")
+    if rows != (M if gather else M * k):
+        raise ValueError("x must have one row per token of the plan" if gather else
+                         "x must have one row per pair of the plan")
+    return N, E, k, M * k
+
+
+def gemm_mxfp4_grouped(x, w, w_scale, plan: MoePlan, epi: int = EPI_NONE, gather: bool = True, out=None):
+    """The experts' products over rows in expert order, y[r] = epi(q(x[src]) @ w[e]^T) with e the expert of row r.
+    gather: x bf16 [M,K] holds the tokens (src = plan.order[r] // top_k), else [P,K] the sorted rows (src = r).
+    w MXFP4 codes [E,N,K/2], w_scale bytes [E,N,K/32].  Returns y bf16 [P,N] (or [P,N/2]); rows without a pair are
+    zeros."""
+    _need_here(x, (torch.bfloat16,), 2, "x")
+    rows, K = x.shape
+    N, E, k, P = _grouped_args(rows, K, w, w_scale, plan, gather)
+    y = _out(out, (P, N // 2 if epi == EPI_SILU_MUL else N), torch.bfloat16, x)
+    _apart(y, "out", w=w, w_scale=w_scale)
+    wsn = int(lib().pq_gemm_mxfp4_grouped_workspace(rows, K, N, epi))
+    ws = torch.empty(wsn, dtype=torch.uint8, device=x.device)
+    _check(lib().pq_gemm_mxfp4_grouped(_p(x), rows, K, _p(plan.order if gather else None), k, _p(plan.offsets), P, E,
+                                       _p(w), _p(w_scale), N, epi, _p(y), _p(ws), wsn, _stream()),
+           "pq_gemm_mxfp4_grouped")
+    return y
+
+
+def gemm_mxfp4_grouped_prequant(xq, xs, w, w_scale, plan: MoePlan, epi: int = EPI_NONE, gather: bool = True,
+                                out=None):
+    """The products of gemm_mxfp4_grouped on rows that quantize_mxfp4 made (xq [rows,K/2], xs [rows,K/32])."""
+    rows, K = _mx_rows(xq, xs)
+    N, E, k, P = _grouped_args(rows, K, w, w_scale, plan, gather)
+    y = _out(out, (P, N // 2 if epi == EPI_SILU_MUL else N), torch.bfloat16, xq)
+    _apart(y, "out", xq=xq, xs=xs, w=w, w_scale=w_scale)
+    _check(lib().pq_gemm_mxfp4_grouped_prequant(_p(xq), _p(xs), rows, K, _p(plan.order if gather else None), k,
+                                                _p(plan.offsets), P, E, _p(w), _p(w_scale), N, epi, _p(y), _stream()),
+           "pq_gemm_mxfp4_grouped_prequant")
+    return y
+
+
+def moe_prefill_layer_mxfp4(x, w13, s13, w2, s2, topk_ids, topk_w, out=None):
+    """One routed MoE layer over any number of tokens, with MXFP4 experts: sort the pairs, gate_up with SiLU*up over
+    the tokens in place, down, and the weighted sum back at the tokens.
+
+    x bf16 [M,H]; w13 codes [E,2I,H/2], s13 bytes [E,2I,H/32] (gate rows, then up rows); w2 codes [E,H,I/2], s2 bytes
+    [E,H,I/32]; topk_ids int32 [M,top_k] (outside [0,E): no expert), topk_w fp32 [M,top_k].  Both products quantise
+    their input live, as moe_decode_layer does.  Returns y bf16 [M,H]."""
+    _need_here(w13, (torch.uint8,), 3, "w13")
+    plan = moe_sort(topk_ids, w13.shape[0])
+    h = gemm_mxfp4_grouped(x, w13, s13, plan, EPI_SILU_MUL)
+    return moe_combine(gemm_mxfp4_grouped(h, w2, s2, plan, gather=False), plan, topk_w, out)

@@ -37,6 +37,22 @@ SIGNATURES = {
     "moe_decode_layer_noalloc": (_c_int, [_vp, _c_int, _c_int, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int,
                                           _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                                           _vp, _vp]),
+    "pq_quantize_mxfp4": (_c_int, [_vp, _c_int, _c_int, _c_int, _vp, _vp, _vp]),
+    "pq_dequantize_mxfp4": (_c_int, [_vp, _vp, _c_int, _c_int, _c_int, _vp, _vp]),
+    "pq_gemv_mxfp4": (_c_int, [_vp, _c_int, _c_int, _vp, _vp, _c_int, _c_int, _vp, _vp]),
+    "pq_gemm_mxfp4_workspace": (_c_size, [_c_int, _c_int, _c_int, _c_int]),
+    "pq_gemm_mxfp4": (_c_int, [_vp, _c_int, _c_int, _vp, _vp, _c_int, _c_int, _vp, _vp, _c_size, _vp]),
+    "pq_gemm_mxfp4_prequant": (_c_int, [_vp, _vp, _c_int, _c_int, _vp, _vp, _c_int, _c_int, _vp, _vp]),
+    "pq_gemm_mxfp4_grouped_workspace": (_c_size, [_c_int, _c_int, _c_int, _c_int]),
+    "pq_gemm_mxfp4_grouped": (_c_int, [_vp, _c_int, _c_int, _vp, _c_int, _vp, _c_int, _c_int, _vp, _vp, _c_int,
+                                       _c_int, _vp, _vp, _c_size, _vp]),
+    "pq_gemm_mxfp4_grouped_prequant": (_c_int, [_vp, _vp, _c_int, _c_int, _vp, _c_int, _vp, _c_int, _c_int, _vp, _vp,
+                                                _c_int, _c_int, _vp, _vp]),
+    "pq_moe_sort_workspace": (_c_size, [_c_int, _c_int, _c_int]),
+    "pq_moe_sort": (_c_int, [_vp, _c_int, _c_int, _c_int, _vp, _vp, _vp, _vp, _c_size, _vp]),
+    "pq_moe_dispatch": (_c_int, [_vp, _c_int, _c_int, _c_int, _c_int, _vp, _vp, _vp, _vp]),
+    "pq_moe_combine": (_c_int, [_vp, _c_int, _c_int, _c_int, _c_int, _vp, _vp, _vp, _vp]),
+    "pq_moe_combine_grad": (_c_int, [_vp, _vp, _c_int, _c_int, _c_int, _c_int, _vp, _vp, _vp, _vp, _vp, _vp]),
     "pq_workspace_init": (_c_int, [_vp, _c_size, _vp]),
     "pq_workspace_check": (_c_int, [_vp, _vp]),
     "pq_strerror": (ctypes.c_char_p, [_c_int]),

@@ -1,0 +1,250 @@
+// MXFP4 weight-streaming GEMV (bf16 activation as it is, M <= 16) with an
+// optional fused SiLU(gate)*up epilogue:
+//   y[m, n] = epi( sum_k x[m,k] 2^(b[n,k/32] - 127) e2m1[n,k] )
+//
+// Bound by the weight stream: 17 bytes for 32 weights.  gfx950 design
+//   * the products run on the matrix cores for every M:
+//     v_mfma_f32_16x16x32_bf16 with 16 weight rows as columns and up to 16
+//     tokens as rows.  The converter turns one byte of codes into a scaled
+//     bf16 pair (exact), so a weight costs half a vector instruction whatever
+//     M is, and the block scales ride along;
+//   * a block owns a contiguous range of output rows, cut into tiles of at
+//     most 16 rows of equal size; the (tile, 256-value step) units are dealt to
+//     its waves as contiguous runs, and tiles cut between waves are added
+//     through LDS in wave order after one barrier: no global partials;
+//   * a wave's load covers 8 rows x 128 bytes (whole lines): lane (g, r)
+//     (g = lane / 16, r = lane % 16) first loads piece g + 4 (r / 8) of row
+//     r % 8, then piece g + 4 (1 - r / 8) of row 8 + r % 8; swapping between
+//     lanes r and r ^ 8 (one row rotation by 8) leaves lane (g, r) with pieces
+//     g and g + 4 of row r, the operand layout;
+//   * x is staged once per block in LDS, rows padded by 16 bytes so that eight
+//     tokens' reads fall on different banks.
+#include "pq_mxfp4_dev.h"
+
+namespace {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float floatx4 __attribute__((ext_vector_type(4)));
+
+constexpr int kThreads = 512;
+constexpr int kWaves = kThreads / pq::kWave;
+constexpr int kMaxM = 16;
+constexpr long kMaxMK = 69632;         // M*K bound: the activation lives in one CU's LDS
+constexpr int kTile = 16;              // weight rows per tile
+constexpr int kStep = 256;             // values of K per step (128 bytes of each row)
+
+struct MxArgs {
+  const uint16_t* x;
+  const uint8_t* w;
+  const uint8_t* wsc;
+  uint16_t* y;
+  int M, K, N, R;       // R: output rows (N, or N/2 under SiLU*up)
+  int nk;               // steps per tile
+  uint32_t xstride;     // LDS bytes of one token's x
+  uint32_t poff;        // LDS offset of the partial sums
+};
+
+__device__ __forceinline__ floatx4 mfma16(uint4 a, uint4 b, floatx4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c,
+                                                 0, 0, 0);
+}
+
+// lane l's dword from lane l ^ 8 (a row rotation by 8)
+__device__ __forceinline__ uint32_t ror8(uint32_t v) { return (uint32_t)pq::dpp_i32<0x128>((int)v); }
+
+// NROW: 2 under SiLU*up (gate row and up row of the same outputs), else 1.
+// D: steps in flight per wave.
+template <int NROW, int D>
+__global__ __launch_bounds__(kThreads) void gemv_mxfp4_kernel(MxArgs a) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int tid = (int)threadIdx.x, lane = pq::lane_id();
+  const int wv = __builtin_amdgcn_readfirstlane(pq::wave_id());
+  const int r16 = lane & 15, g = lane >> 4;
+
+  // this block's rows and this wave's run of units
+  const int rs = pq::split_start(a.R, (int)gridDim.x, (int)blockIdx.x);
+  const int rows = pq::split_start(a.R, (int)gridDim.x, (int)blockIdx.x + 1) - rs;
+  const int nt = (rows + kTile - 1) / kTile;             // tiles; tile t: rows split(rows, nt, t) ..
+  const int U = nt * a.nk;
+  const int u0 = pq::split_start(U, kWaves, wv);
+  const int left0 = pq::split_start(U, kWaves, wv + 1) - u0;
+
+  const uint32_t rowb = (uint32_t)(a.K / 2), nsc = (uint32_t)(a.K / pq::kMxBlock);
+  const pq::rsrc_t wr = pq::make_rsrc(a.w, (uint32_t)((size_t)a.N * rowb));
+  const pq::rsrc_t sr = pq::make_rsrc(a.wsc, (uint32_t)((size_t)a.N * nsc));
+
+  // ring of weight loads
+  const int lrow = r16 & 7, up8 = r16 >> 3;
+  int it = nt > 0 ? u0 / a.nk : 0, ik = nt > 0 ? u0 - it * a.nk : 0, ileft = left0;
+  auto issue = [&](uint4 (&wb)[NROW][2], uint32_t (&sb)[NROW][2]) {
+    const bool ok = ileft > 0;
+    const int t0 = ok ? pq::split_start(rows, nt, it) : 0;
+    const int tn = ok ? pq::split_start(rows, nt, it + 1) - t0 : 0;
+    const uint32_t p0 = (uint32_t)(8 * ik + g + 4 * up8), p1 = (uint32_t)(8 * ik + g + 4 * (1 - up8));
+    const uint32_t q0 = (uint32_t)(8 * ik + g);
+#pragma unroll
+    for (int j = 0; j < NROW; ++j) {
+      const uint32_t base = (uint32_t)(rs + t0 + j * a.R);
+      wb[j][0] = pq::buf_load16_nt(wr, lrow < tn && p0 < nsc ? (base + lrow) * rowb + 16u * p0 : pq::kOOB);
+      wb[j][1] = pq::buf_load16_nt(wr, lrow + 8 < tn && p1 < nsc ? (base + 8 + lrow) * rowb + 16u * p1 : pq::kOOB);
+      const uint32_t so = (base + (uint32_t)r16) * nsc + q0;
+      sb[j][0] = __builtin_amdgcn_raw_buffer_load_b8(sr, (int)(r16 < tn && q0 < nsc ? so : pq::kOOB), 0, 0);
+      sb[j][1] = __builtin_amdgcn_raw_buffer_load_b8(sr, (int)(r16 < tn && q0 + 4 < nsc ? so + 4u : pq::kOOB), 0, 0);
+    }
+    --ileft;
+    if (++ik == a.nk) { ik = 0; ++it; }
+  };
+  uint4 wbuf[D][NROW][2];
+  uint32_t sbuf[D][NROW][2];
+#pragma unroll
+  for (int d = 0; d < D; ++d) issue(wbuf[d], sbuf[d]);
+  __builtin_amdgcn_sched_barrier(0);
+
+  // x into LDS: token m's row at m * xstride, and a block of zeros that stands
+  // for the blocks of the last step past K (their weights read as zero, but a
+  // product with another token's infinity would not be)
+  {
+    const int pieces = a.K / 8;                          // 16-byte pieces per token
+    for (int i = tid; i < a.M * pieces; i += kThreads) {
+      const int m = i / pieces, p = i - m * pieces;
+      *reinterpret_cast<uint4*>(smem + (uint32_t)m * a.xstride + 16u * (uint32_t)p) =
+          reinterpret_cast<const uint4*>(a.x)[i];
+    }
+    if (tid < 4) *reinterpret_cast<uint4*>(smem + a.poff - 64u + 16u * (uint32_t)tid) = make_uint4(0u, 0u, 0u, 0u);
+  }
+  __syncthreads();
+
+  // A row r16 is token r16 % M (rows past M repeat tokens; their results are not used)
+  const uint32_t xl = (uint32_t)(r16 % a.M) * a.xstride;
+  float* part = reinterpret_cast<float*>(smem + a.poff); // [nt + kWaves][NROW][16 rows][16 tokens]
+  floatx4 acc[NROW];
+#pragma unroll
+  for (int j = 0; j < NROW; ++j) acc[j] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+  int ct = nt > 0 ? u0 / a.nk : 0, ck = nt > 0 ? u0 - ct * a.nk : 0, cleft = left0;
+
+  auto consume = [&](const uint4 (&wb)[NROW][2], const uint32_t (&sb)[NROW][2]) {
+    uint4 xa[2][4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t blk = (uint32_t)(8 * ck + 4 * h + g);
+      const uint8_t* xp = smem + (blk < nsc ? xl + 64u * blk : a.poff - 64u);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) xa[h][t] = *reinterpret_cast<const uint4*>(xp + 16 * t);
+    }
+#pragma unroll
+    for (int j = 0; j < NROW; ++j) {
+      const uint32_t v0[4] = {wb[j][0].x, wb[j][0].y, wb[j][0].z, wb[j][0].w};
+      const uint32_t v1[4] = {wb[j][1].x, wb[j][1].y, wb[j][1].z, wb[j][1].w};
+      const float s0 = pq::mx_scale_operand(sb[j][0]), s1 = pq::mx_scale_operand(sb[j][1]);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const uint32_t lo = up8 ? v1[t] : v0[t];          // piece g of row r16
+        const uint32_t hi = ror8(up8 ? v0[t] : v1[t]);    // piece g + 4, from lane r16 ^ 8
+        acc[j] = mfma16(xa[0][t], pq::mx_bf16x8(lo, s0), acc[j]);
+        acc[j] = mfma16(xa[1][t], pq::mx_bf16x8(hi, s1), acc[j]);
+      }
+    }
+    --cleft;
+    if (++ck == a.nk || cleft == 0) {                     // this wave's part of the tile
+      // a wave's parts are slots ct + wv: later waves start at the same or a later tile
+#pragma unroll
+      for (int j = 0; j < NROW; ++j)
+        *reinterpret_cast<floatx4*>(part + ((size_t)((ct + wv) * NROW + j) * 16 + r16) * 16 + 4 * g) = acc[j];
+#pragma unroll
+      for (int j = 0; j < NROW; ++j) acc[j] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+    if (ck == a.nk) { ck = 0; ++ct; }
+  };
+
+  int base = 0;
+  for (; base + D < left0; base += D) {
+#pragma unroll
+    for (int q = 0; q < D; ++q) {
+      consume(wbuf[q], sbuf[q]);
+      issue(wbuf[q], sbuf[q]);
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < D; ++q)
+    if (base + q < left0) consume(wbuf[q], sbuf[q]);
+  __syncthreads();
+
+  // outputs: the parts of a tile in wave order
+  const int q = U / kWaves, rem = U - q * kWaves;
+  for (int i = tid; i < rows * a.M; i += kThreads) {
+    const int m = i / rows, r = i - m * rows;
+    // tile of row r, and its first row
+    const int tq = rows / nt, tr = rows - tq * nt;
+    const int t = r < tr * (tq + 1) ? r / (tq + 1) : tr + (r - tr * (tq + 1)) / tq;
+    const int rl = r - pq::split_start(rows, nt, t);
+    // waves that hold units t nk .. (t + 1) nk - 1
+    auto wave_of = [&](int u) { return u < rem * (q + 1) ? u / (q + 1) : rem + (u - rem * (q + 1)) / q; };
+    const int w0 = wave_of(t * a.nk), w1 = wave_of((t + 1) * a.nk - 1);
+    float v[NROW];
+#pragma unroll
+    for (int j = 0; j < NROW; ++j) v[j] = 0.0f;
+    for (int w = w0; w <= w1; ++w)
+#pragma unroll
+      for (int j = 0; j < NROW; ++j) v[j] += part[((size_t)((t + w) * NROW + j) * 16 + rl) * 16 + m];
+    a.y[(size_t)m * a.R + rs + r] = pq::bf16_rne(NROW == 2 ? pq::silu_mul_f32(v[0], v[NROW - 1]) : v[0]);
+  }
+}
+
+constexpr size_t kMaxLds = 160 * 1024;
+
+template <int NROW, int D>
+hipError_t launch(const MxArgs& a, size_t lds, int grid, hipStream_t stream) {
+  auto kern = gemv_mxfp4_kernel<NROW, D>;
+  static pqhost::KernelAttrOnce attr;
+  const hipError_t e = pqhost::set_dynamic_lds_once(attr, (const void*)kern, (int)kMaxLds);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(kThreads), lds, stream, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+extern "C" {
+
+int pq_gemv_mxfp4(const uint16_t* x, int M, int K, const uint8_t* w, const uint8_t* w_scale, int N, int epi,
+                  uint16_t* y, void* stream) {
+  if (!x || !w || !w_scale || !y) return PQ_ERR_NULL;
+  if (M < 1 || M > kMaxM || K < pq::kMxBlock || K % pq::kMxBlock != 0 || N < 1) return PQ_ERR_SHAPE;
+  if (epi != PQ_EPI_NONE && epi != PQ_EPI_SILU_MUL) return PQ_ERR_SHAPE;
+  const int silu = epi == PQ_EPI_SILU_MUL;
+  if (silu && N % 2 != 0) return PQ_ERR_SHAPE;
+  if ((long)M * K > kMaxMK || (size_t)N * (K / 2) > pq::kMaxBufferBytes) return PQ_ERR_SHAPE;
+  if (!pqhost::aligned16(x) || !pqhost::aligned16(w) || !pqhost::aligned16(w_scale) || !pqhost::aligned16(y))
+    return PQ_ERR_ALIGN;
+  pqhost::DeviceInfo dev;
+  const int st = pqhost::current_device_info(&dev);
+  if (st != PQ_OK) return st;
+  MxArgs a;
+  a.x = x; a.w = w; a.wsc = w_scale; a.y = y;
+  a.M = M; a.K = K; a.N = N;
+  a.R = silu ? N / 2 : N;
+  a.nk = (K + kStep - 1) / kStep;
+  a.xstride = (uint32_t)K * 2 + 16;
+  a.poff = (uint32_t)M * a.xstride + 64;
+  // one block per CU, more where a block's partial sums would not fit its LDS
+  const int nrow = silu ? 2 : 1;
+  int grid = dev.num_cus;
+  size_t lds;
+  for (;; grid *= 2) {
+    const int rows = (a.R + grid - 1) / grid;
+    const int nt = (rows + kTile - 1) / kTile;
+    lds = a.poff + (size_t)(nt + kWaves) * nrow * 16 * 16 * 4;
+    if (lds <= kMaxLds || rows <= kTile) break;
+  }
+  if (lds > kMaxLds) return PQ_ERR_SHAPE;
+  if (grid > a.R) grid = a.R;
+  const hipError_t e = silu ? launch<2, 2>(a, lds, grid, (hipStream_t)stream)
+                            : launch<1, 3>(a, lds, grid, (hipStream_t)stream);
+  if (e != hipSuccess) {
+    pqhost::set_last_hip_error((int)e);
+    return PQ_ERR_HIP;
+  }
+  return PQ_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,403 @@
+// The (token, slot) pairs of a routed batch put in expert order, the tokens'
+// rows moved there and back, and the gradients of both moves.
+//
+//   sort     order[r] = the pair at sorted row r, inverse[p] = the row of pair
+//            p, offsets[e] = expert e's first row; pairs of one expert stay in
+//            pair order.  A counting sort: ranks from counts, no atomics whose
+//            order could show.
+//   dispatch xs[r] = x[order[r] / k]
+//   combine  y[m] = sum_s w[m,s] ys[inverse[m,s]]     (w = 1: the gradient of dispatch)
+//   grad     dys[r] = w[p] dy[p / k], dw[p] = <dy[p / k], ys[r]> with p = order[r]
+//
+// The sort is bound by latency (a few launches over a few hundred KB); the
+// moves by memory, each row read and written once.  All of them go by tokens,
+// not by sorted rows, so a token's row comes from HBM once for its k uses.
+#include "pq_common.h"
+
+namespace {
+
+// ---------------------------------------------------------------------------
+// sort
+// ---------------------------------------------------------------------------
+constexpr int kSortThreads = 1024;
+constexpr int kSortWaves = kSortThreads / pq::kWave;
+constexpr int kMaxExperts = 1024;          // one thread per expert in the scans
+constexpr int kSortChunk = 2048;           // least pairs per block
+constexpr int kMaxSortBlocks = 256;        // every block adds up the counts of all blocks
+
+struct SortArgs {
+  const int32_t* ids;
+  int P, E;
+  int chunk;                               // pairs per block, a multiple of kSortThreads
+  int nb;                                  // blocks
+  int ebits;                               // bits of an expert id
+  int32_t *order, *inverse, *offsets;
+  uint32_t* hist;                          // [nb][E] counts (nb > 1)
+};
+
+__global__ __launch_bounds__(kSortThreads) void moe_count_kernel(SortArgs a) {
+  __shared__ uint32_t cnt[kMaxExperts];
+  const int tid = (int)threadIdx.x;
+  if (tid < a.E) cnt[tid] = 0;
+  __syncthreads();
+  const long p0 = (long)blockIdx.x * a.chunk;
+  for (int i = tid; i < a.chunk; i += kSortThreads) {
+    if (p0 + i >= a.P) break;
+    const uint32_t e = (uint32_t)a.ids[p0 + i];
+    if (e < (uint32_t)a.E) atomicAdd(&cnt[e], 1u);         // a count does not depend on the order
+  }
+  __syncthreads();
+  if (tid < a.E) a.hist[(size_t)blockIdx.x * a.E + tid] = cnt[tid];
+}
+
+// Lanes of the wave with the same key (key < 2^bits), among the lanes of `live`.
+__device__ __forceinline__ uint64_t same_key(uint32_t key, int bits, uint64_t live) {
+  uint64_t m = live;
+  for (int b = 0; b < bits; ++b) {
+    const bool one = (key >> b) & 1u;
+    const uint64_t v = __ballot(one);
+    m &= one ? v : ~v;
+  }
+  return m;
+}
+
+__global__ __launch_bounds__(kSortThreads) void moe_sort_kernel(SortArgs a) {
+  extern __shared__ uint32_t pos[];                        // [kSortWaves][E]: next row of a wave's pairs
+  __shared__ uint32_t wsum[kSortWaves];
+  __shared__ uint32_t s_total;
+  const int tid = (int)threadIdx.x, lane = pq::lane_id(), wv = pq::wave_id();
+  const int E = a.E, b = (int)blockIdx.x;
+  for (int i = tid; i < kSortWaves * E; i += kSortThreads) pos[i] = 0;
+  __syncthreads();
+  // counts of each wave's run of pairs
+  const int seg = a.chunk / kSortWaves;
+  const long p0 = (long)b * a.chunk + (long)wv * seg;
+  uint32_t* mine = pos + wv * E;
+  for (int i = lane; i < seg; i += pq::kWave) {
+    if (p0 + i >= a.P) break;
+    const uint32_t e = (uint32_t)a.ids[p0 + i];
+    if (e < (uint32_t)E) atomicAdd(&mine[e], 1u);
+  }
+  __syncthreads();
+  // thread e: the expert's pairs in all blocks and in the blocks before this one
+  uint32_t total = 0, before = 0;
+  if (tid < E) {
+    if (a.nb > 1) {
+      for (int i = 0; i < a.nb; ++i) {
+        const uint32_t c = a.hist[(size_t)i * E + tid];
+        total += c;
+        before += i < b ? c : 0u;
+      }
+    } else {
+      for (int w = 0; w < kSortWaves; ++w) total += pos[w * E + tid];
+    }
+  }
+  // exclusive scan of the totals over the experts
+  uint32_t inc = total;
+#pragma unroll
+  for (int d = 1; d < pq::kWave; d <<= 1) {
+    const uint32_t o = __shfl_up(inc, d, pq::kWave);
+    inc += lane >= d ? o : 0u;
+  }
+  if (lane == pq::kWave - 1) wsum[wv] = inc;
+  __syncthreads();
+  uint32_t first = inc - total;
+  for (int w = 0; w < wv; ++w) first += wsum[w];
+  if (tid == kSortThreads - 1) s_total = first + total;
+  if (tid < E) {
+    if (b == 0) {
+      a.offsets[tid] = (int32_t)first;
+      if (tid == E - 1) a.offsets[E] = (int32_t)(first + total);
+    }
+    uint32_t at = first + before;
+    for (int w = 0; w < kSortWaves; ++w) {                 // counts become each wave's first row
+      const uint32_t c = pos[w * E + tid];
+      pos[w * E + tid] = at;
+      at += c;
+    }
+  }
+  __syncthreads();
+  for (int i = 0; i < seg; i += pq::kWave) {               // the whole wave together: seg is a multiple of 64
+    const long p = p0 + i + lane;
+    const bool in = p < a.P;
+    const uint32_t e = in ? (uint32_t)a.ids[p] : 0xffffffffu;
+    const bool has = e < (uint32_t)E;
+    const uint64_t m = same_key(has ? e : 0u, a.ebits, __ballot(has));
+    const int rank = __popcll(m & ((1ull << lane) - 1ull));
+    int r = -1;
+    if (has) r = (int)(mine[e] + (uint32_t)rank);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // every lane has read before the counts move on
+    __builtin_amdgcn_wave_barrier();
+    if (has && rank == 0) mine[e] += (uint32_t)__popcll(m);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    if (in) {
+      a.inverse[p] = r;
+      if (has) a.order[r] = (int32_t)p;
+    }
+  }
+  // rows behind the last pair with an expert: this block's share of them
+  const long r0 = (long)b * a.chunk;
+  for (int i = tid; i < a.chunk; i += kSortThreads)
+    if (r0 + i < a.P && (uint32_t)(r0 + i) >= s_total) a.order[r0 + i] = -1;
+}
+
+// ---------------------------------------------------------------------------
+// moves
+// ---------------------------------------------------------------------------
+constexpr int kMoveThreads = 256;
+
+struct MoveArgs {
+  const uint8_t* src;
+  uint8_t* dst;
+  const int32_t *order, *inverse;
+  const float* w;          // combine: weights [P], or null for 1
+  int M, k, P;
+  int n16;                 // 16-byte pieces of a row
+};
+
+// Block (c, m): pieces 256 c .. of token m's row, to its k sorted rows; and of
+// the sorted rows m k .. m k + k - 1 those that no pair takes, as zeros.
+__global__ __launch_bounds__(kMoveThreads) void moe_dispatch_kernel(MoveArgs a) {
+  const int c = (int)blockIdx.x * kMoveThreads + (int)threadIdx.x;
+  if (c >= a.n16) return;
+  for (long m = blockIdx.y; m < a.M; m += gridDim.y) {
+    const uint4 v = reinterpret_cast<const uint4*>(a.src)[(size_t)m * a.n16 + c];
+    for (int s = 0; s < a.k; ++s) {
+      const long p = m * a.k + s;
+      const int r = a.inverse[p];
+      if ((uint32_t)r < (uint32_t)a.P) reinterpret_cast<uint4*>(a.dst)[(size_t)r * a.n16 + c] = v;
+      if (a.order[p] < 0) reinterpret_cast<uint4*>(a.dst)[(size_t)p * a.n16 + c] = make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
+}
+
+template <bool F32>
+struct Piece {                                   // 16 bytes of a row as fp32 values
+  static constexpr int N = F32 ? 4 : 8;
+  float v[N];
+  __device__ __forceinline__ void set(uint4 r) {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (F32) {
+        v[i] = __uint_as_float(w[i]);
+      } else {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      }
+    }
+  }
+  __device__ __forceinline__ uint4 get() const {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (F32) w[i] = __float_as_uint(v[i]);
+      else w[i] = (uint32_t)pq::bf16_rne(v[2 * i]) | ((uint32_t)pq::bf16_rne(v[2 * i + 1]) << 16);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+
+// Block (c, m): pieces 256 c .. of token m: its k sorted rows, weighted, added
+// in fp32 in slot order and rounded once.
+template <bool F32>
+__global__ __launch_bounds__(kMoveThreads) void moe_combine_kernel(MoveArgs a) {
+  const int c = (int)blockIdx.x * kMoveThreads + (int)threadIdx.x;
+  if (c >= a.n16) return;
+  for (long m = blockIdx.y; m < a.M; m += gridDim.y) {
+    Piece<F32> acc;
+#pragma unroll
+    for (int i = 0; i < Piece<F32>::N; ++i) acc.v[i] = 0.0f;
+    for (int s = 0; s < a.k; ++s) {
+      const long p = m * a.k + s;
+      const int r = a.inverse[p];
+      if ((uint32_t)r >= (uint32_t)a.P) continue;
+      const float w = a.w ? a.w[p] : 1.0f;
+      Piece<F32> v;
+      v.set(reinterpret_cast<const uint4*>(a.src)[(size_t)r * a.n16 + c]);
+#pragma unroll
+      for (int i = 0; i < Piece<F32>::N; ++i) acc.v[i] = fmaf(w, v.v[i], acc.v[i]);
+    }
+    reinterpret_cast<uint4*>(a.dst)[(size_t)m * a.n16 + c] = acc.get();
+  }
+}
+
+struct GradArgs {
+  const uint8_t *dy, *ys;
+  uint8_t* dys;
+  float* dw;
+  const int32_t *order, *inverse;
+  const float* w;
+  int k, P, n16;
+};
+
+// One wave per pair: dys[r] = w dy, dw = <dy, ys[r]>.
+template <bool F32>
+__global__ __launch_bounds__(512) void moe_combine_grad_kernel(GradArgs a) {
+  const int lane = pq::lane_id();
+  const uint4* dy = reinterpret_cast<const uint4*>(a.dy);
+  const uint4* ys = reinterpret_cast<const uint4*>(a.ys);
+  uint4* dys = reinterpret_cast<uint4*>(a.dys);
+  for (long p = (long)blockIdx.x * 8 + pq::wave_id(); p < a.P; p += (long)gridDim.x * 8) {
+    const int r = __builtin_amdgcn_readfirstlane(a.inverse[p]);
+    if (__builtin_amdgcn_readfirstlane(a.order[p]) < 0)          // sorted row p that no pair takes
+      for (int c = lane; c < a.n16; c += pq::kWave) dys[(size_t)p * a.n16 + c] = make_uint4(0u, 0u, 0u, 0u);
+    float sum = 0.0f;
+    if ((uint32_t)r < (uint32_t)a.P) {
+      const float w = a.w[p];
+      const size_t m = (size_t)(p / a.k);
+      for (int c = lane; c < a.n16; c += pq::kWave) {
+        Piece<F32> g, v;
+        g.set(dy[m * a.n16 + c]);
+        v.set(ys[(size_t)r * a.n16 + c]);
+#pragma unroll
+        for (int i = 0; i < Piece<F32>::N; ++i) {
+          sum = fmaf(g.v[i], v.v[i], sum);
+          g.v[i] *= w;
+        }
+        dys[(size_t)r * a.n16 + c] = g.get();
+      }
+    }
+    sum = pq::wave_sum(sum);
+    if (lane == 0) a.dw[p] = sum;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+void sort_plan(int P, int* chunk, int* nb) {
+  long c = kSortChunk;
+  if ((long)P > c * kMaxSortBlocks) c = ((long)P / kMaxSortBlocks / kSortThreads + 1) * kSortThreads;
+  *chunk = (int)c;
+  *nb = (int)(((long)P + c - 1) / c);
+}
+
+bool sort_shape_ok(int M, int top_k, int E) {
+  return M >= 1 && top_k >= 1 && E >= 1 && E <= kMaxExperts && (long)M * top_k < (1l << 31);
+}
+
+int row_pieces(int H, int is_f32, int* n16) {
+  if (H < 8 || H % 8 != 0) return PQ_ERR_SHAPE;
+  *n16 = is_f32 ? H / 4 : H / 8;
+  return PQ_OK;
+}
+
+dim3 move_grid(int n16, int M) {
+  // grid.y is at most 65535: the kernels loop over further tokens
+  return dim3((unsigned)((n16 + kMoveThreads - 1) / kMoveThreads), (unsigned)(M < 65535 ? M : 65535));
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t pq_moe_sort_workspace(int M, int top_k, int E) {
+  if (!sort_shape_ok(M, top_k, E)) return 0;
+  int chunk, nb;
+  sort_plan(M * top_k, &chunk, &nb);
+  return nb > 1 ? pq::kWsDataOff + pqhost::align_up((size_t)nb * E * 4, 256) : 0;
+}
+
+int pq_moe_sort(const int32_t* topk_ids, int M, int top_k, int E, int32_t* order, int32_t* inverse,
+                int32_t* offsets, void* ws, size_t ws_bytes, void* stream) {
+  if (!topk_ids || !order || !inverse || !offsets) return PQ_ERR_NULL;
+  if (!sort_shape_ok(M, top_k, E)) return PQ_ERR_SHAPE;
+  if (!pqhost::aligned16(topk_ids) || !pqhost::aligned16(order) || !pqhost::aligned16(inverse) ||
+      !pqhost::aligned16(offsets) || (ws && !pqhost::aligned16(ws)))
+    return PQ_ERR_ALIGN;
+  const size_t need = pq_moe_sort_workspace(M, top_k, E);
+  if (need && (!ws || ws_bytes < need)) return PQ_ERR_WORKSPACE;
+  pqhost::DeviceInfo dev;
+  const int st = pqhost::current_device_info(&dev);
+  if (st != PQ_OK) return st;
+  SortArgs a;
+  a.ids = topk_ids;
+  a.P = M * top_k;
+  a.E = E;
+  sort_plan(a.P, &a.chunk, &a.nb);
+  a.ebits = 0;
+  while ((1 << a.ebits) < E) ++a.ebits;
+  a.order = order; a.inverse = inverse; a.offsets = offsets;
+  a.hist = need ? reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(ws) + pq::kWsDataOff) : nullptr;
+  if (a.nb > 1) {
+    hipLaunchKernelGGL(moe_count_kernel, dim3((unsigned)a.nb), dim3(kSortThreads), 0, (hipStream_t)stream, a);
+    PQ_HIP_CHECK(hipGetLastError());
+  }
+  static pqhost::KernelAttrOnce attr;
+  PQ_HIP_CHECK(pqhost::set_dynamic_lds_once(attr, (const void*)moe_sort_kernel, kSortWaves * kMaxExperts * 4));
+  hipLaunchKernelGGL(moe_sort_kernel, dim3((unsigned)a.nb), dim3(kSortThreads), (size_t)kSortWaves * E * 4,
+                     (hipStream_t)stream, a);
+  PQ_HIP_CHECK(hipGetLastError());
+  return PQ_OK;
+}
+
+int pq_moe_dispatch(const void* x, int is_f32, int M, int H, int top_k, const int32_t* order,
+                    const int32_t* inverse, void* xs, void* stream) {
+  if (!x || !order || !inverse || !xs) return PQ_ERR_NULL;
+  MoveArgs a;
+  if (!sort_shape_ok(M, top_k, 1) || row_pieces(H, is_f32, &a.n16) != PQ_OK) return PQ_ERR_SHAPE;
+  if (!pqhost::aligned16(x) || !pqhost::aligned16(xs) || !pqhost::aligned16(order) || !pqhost::aligned16(inverse))
+    return PQ_ERR_ALIGN;
+  pqhost::DeviceInfo dev;
+  const int st = pqhost::current_device_info(&dev);
+  if (st != PQ_OK) return st;
+  a.src = (const uint8_t*)x;
+  a.dst = (uint8_t*)xs;
+  a.order = order; a.inverse = inverse; a.w = nullptr;
+  a.M = M; a.k = top_k; a.P = M * top_k;
+  hipLaunchKernelGGL(moe_dispatch_kernel, move_grid(a.n16, M), dim3(kMoveThreads), 0, (hipStream_t)stream, a);
+  PQ_HIP_CHECK(hipGetLastError());
+  return PQ_OK;
+}
+
+int pq_moe_combine(const void* ys, int is_f32, int M, int H, int top_k, const int32_t* inverse,
+                   const float* topk_w, void* y, void* stream) {
+  if (!ys || !inverse || !y) return PQ_ERR_NULL;
+  MoveArgs a;
+  if (!sort_shape_ok(M, top_k, 1) || row_pieces(H, is_f32, &a.n16) != PQ_OK) return PQ_ERR_SHAPE;
+  if (!pqhost::aligned16(ys) || !pqhost::aligned16(y) || !pqhost::aligned16(inverse) ||
+      (topk_w && !pqhost::aligned16(topk_w)))
+    return PQ_ERR_ALIGN;
+  pqhost::DeviceInfo dev;
+  const int st = pqhost::current_device_info(&dev);
+  if (st != PQ_OK) return st;
+  a.src = (const uint8_t*)ys;
+  a.dst = (uint8_t*)y;
+  a.order = nullptr; a.inverse = inverse; a.w = topk_w;
+  a.M = M; a.k = top_k; a.P = M * top_k;
+  if (is_f32)
+    hipLaunchKernelGGL(moe_combine_kernel<true>, move_grid(a.n16, M), dim3(kMoveThreads), 0, (hipStream_t)stream, a);
+  else
+    hipLaunchKernelGGL(moe_combine_kernel<false>, move_grid(a.n16, M), dim3(kMoveThreads), 0, (hipStream_t)stream, a);
+  PQ_HIP_CHECK(hipGetLastError());
+  return PQ_OK;
+}
+
+int pq_moe_combine_grad(const void* dy, const void* ys, int is_f32, int M, int H, int top_k, const int32_t* order,
+                        const int32_t* inverse, const float* topk_w, void* dys, float* dw, void* stream) {
+  if (!dy || !ys || !order || !inverse || !topk_w || !dys || !dw) return PQ_ERR_NULL;
+  GradArgs a;
+  if (!sort_shape_ok(M, top_k, 1) || row_pieces(H, is_f32, &a.n16) != PQ_OK) return PQ_ERR_SHAPE;
+  if (!pqhost::aligned16(dy) || !pqhost::aligned16(ys) || !pqhost::aligned16(order) || !pqhost::aligned16(inverse) ||
+      !pqhost::aligned16(topk_w) || !pqhost::aligned16(dys) || !pqhost::aligned16(dw))
+    return PQ_ERR_ALIGN;
+  pqhost::DeviceInfo dev;
+  const int st = pqhost::current_device_info(&dev);
+  if (st != PQ_OK) return st;
+  a.dy = (const uint8_t*)dy; a.ys = (const uint8_t*)ys;
+  a.dys = (uint8_t*)dys; a.dw = dw;
+  a.order = order; a.inverse = inverse; a.w = topk_w;
+  a.k = top_k; a.P = M * top_k;
+  const long blocks = ((long)a.P + 7) / 8;
+  const dim3 grid((unsigned)(blocks < (1 << 20) ? blocks : (1 << 20)));
+  if (is_f32)
+    hipLaunchKernelGGL(moe_combine_grad_kernel<true>, grid, dim3(512), 0, (hipStream_t)stream, a);
+  else
+    hipLaunchKernelGGL(moe_combine_grad_kernel<false>, grid, dim3(512), 0, (hipStream_t)stream, a);
+  PQ_HIP_CHECK(hipGetLastError());
+  return PQ_OK;
+}
+
+}  // extern "C"

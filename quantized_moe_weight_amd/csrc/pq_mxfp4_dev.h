@@ -1,0 +1,53 @@
+// MXFP4 device helpers: blocks of 32 values of a row share one E8M0 scale byte
+// b (the scale 2^(b - 127), 255 = NaN); a value is a 4-bit E2M1 code (sign,
+// then 0 .5 1 1.5 2 3 4 6), two to a byte, low nibble = even k.
+#pragma once
+
+#include "pq_common.h"
+
+namespace pq {
+
+constexpr int kMxBlock = 32;       // values per scale byte
+constexpr uint32_t kMxNan = 255;   // scale byte of a block that holds a value that is not finite
+
+// Scale byte of a block from the bits of its largest magnitude: 2^2 is the
+// largest power of two among the E2M1 levels, so the block's scale is
+// 2^(floor(log2 amax) - 2), no smaller than 2^-127; 1 for a block of zeros.
+// The exponent field of amax is floor(log2 amax) + 127 (0 for subnormals,
+// whose scale is 2^-127 all the same).
+__device__ __forceinline__ uint32_t mx_scale_byte(uint32_t amax_bits) {
+  if (amax_bits >= 0x7f800000u) return kMxNan;
+  if (amax_bits == 0u) return 127u;
+  const uint32_t e = amax_bits >> 23;
+  return e > 2u ? e - 2u : 0u;
+}
+
+// The converters read the exponent field of their fp32 scale operand as the
+// E8M0 byte (field 0 is 2^-127, field 255 is NaN): checked on MI355X for all
+// 256 bytes and 16 codes, and the encoder against the rounding rule for every
+// finite fp32 value at eight scales.
+__device__ __forceinline__ float mx_scale_operand(uint32_t byte) { return __uint_as_float(byte << 23); }
+
+// Codes of 8 values (nearest level, ties to the even code, saturating at 6),
+// value i in nibble i.
+__device__ __forceinline__ uint32_t mx_codes8(const float (&v)[8], float scale) {
+  uint32_t w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, v[0], v[1], scale, 0);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[2], v[3], scale, 1);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[4], v[5], scale, 2);
+  return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[6], v[7], scale, 3);
+}
+
+// 8 codes -> 4 bf16 pairs in k order, scaled (exact; past bf16's range, which
+// only the bytes 253 and 254 reach, infinite)
+__device__ __forceinline__ uint4 mx_bf16x8(uint32_t w, float scale) {
+  uint4 r;
+  r.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 0));
+  r.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 1));
+  r.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 2));
+  r.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 3));
+  return r;
+}
+
+__device__ __forceinline__ float silu_mul_f32(float g, float u) { return g / (1.0f + __expf(-g)) * u; }
+
+}  // namespace pq

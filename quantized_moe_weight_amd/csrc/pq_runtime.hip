@@ -63,12 +63,18 @@ int pq_last_hip_error(void) { return pqhost::g_last_hip_error; }
 
 int pq_launches_per_call(const char* entry_point) {
   if (entry_point == nullptr) return PQ_ERR_NULL;
-  // pq_gemm_fp8 quantises the activation in a launch of its own before the
-  // GEMM; every other compute entry point is one launch
+  // the GEMMs quantise the activation in a launch of its own first, and the
+  // sort of a larger batch counts before it sorts; every other compute entry
+  // point is one launch
   static const char* const kOne[] = {"pq_quantize_fp8", "pq_quantize_q4", "pq_gemv_fp8", "pq_gemm_fp8_prequant",
                                      "pq_gemv_q4", "moe_decode_layer", "moe_decode_layer_ex",
-                                     "moe_decode_layer_noalloc", "pq_stream_probe"};
-  if (strcmp(entry_point, "pq_gemm_fp8") == 0) return 2;
+                                     "moe_decode_layer_noalloc", "pq_stream_probe", "pq_quantize_mxfp4",
+                                     "pq_dequantize_mxfp4", "pq_gemv_mxfp4", "pq_gemm_mxfp4_prequant",
+                                     "pq_gemm_mxfp4_grouped_prequant", "pq_moe_dispatch", "pq_moe_combine",
+                                     "pq_moe_combine_grad"};
+  static const char* const kTwo[] = {"pq_gemm_fp8", "pq_gemm_mxfp4", "pq_gemm_mxfp4_grouped", "pq_moe_sort"};
+  for (const char* n : kTwo)
+    if (strcmp(entry_point, n) == 0) return 2;
   for (const char* n : kOne)
     if (strcmp(entry_point, n) == 0) return 1;
   return PQ_ERR_UNSUPPORTED;
