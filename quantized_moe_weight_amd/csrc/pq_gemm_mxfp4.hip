@@ -6,6 +6,26 @@
 // v_mfma_scale_f32_16x16x128_f8f6f4 takes both operands as E2M1 codes with an
 // E8M0 scale per 32 values: lane l carries row l % 16 and the 32 values (16
 // bytes) and the scale of block l / 16, so the scales cost no vector work.
+//
+// Two kernels.  The tiled one (K % 128 == 0, so that scale rows are whole
+// dwords):
+//   * a 512-thread block (8 waves, 2 along the rows x 4 along the columns) owns
+//     a BM x 256 tile, BM = 256, 128, 64 or 32; a K step is 256 values, 128
+//     bytes of each row: whole lines;
+//   * codes and scales stream from memory straight into LDS (buffer loads with
+//     an LDS destination), S stages deep, one block barrier per step; the wait
+//     leaves the younger stages in flight.  The 16-byte piece c of row r lands
+//     in slot c ^ (r % 8), which spreads the operand reads over all banks;
+//   * in the two matrix instructions of a step lane group g takes pieces 2g and
+//     2g + 1 (the order of K within a sum is free): its two scale bytes are one
+//     16-bit LDS read, and the instruction picks the byte;
+//   * tiles are dealt to the 8 XCDs in contiguous runs of an order that goes
+//     through 8 row tiles before the next column tile, so that blocks sharing
+//     an operand share an L2.  Blocks are persistent: the experts' tile table
+//     is made once per block.
+// The plain one takes any K % 32 == 0: operands straight from memory.
+#include <stdlib.h>
+
 #include "pq_mxfp4_dev.h"
 
 extern "C" int pq_quantize_mxfp4(const void* in, int in_is_f32, int rows, int K, uint8_t* codes, uint8_t* scales,
@@ -16,9 +36,14 @@ namespace {
 typedef int int32x8 __attribute__((ext_vector_type(8)));
 typedef float floatx4 __attribute__((ext_vector_type(4)));
 
-constexpr int kThreads = 256;
 constexpr int kMaxExperts = 1024;
-constexpr int BM = 64, BN = 64;        // tile: 4 waves, 2 x 2, 32 x 32 each
+constexpr int kThreads = 512;          // tiled kernel
+constexpr int BN = 256;
+constexpr int kRowBytes = 128;         // one K step of a row
+constexpr int kXcds = 8;
+constexpr int kGroupM = 8;             // row tiles gone through before the next column tile
+// plain kernel: 4 waves, 2 x 2, 32 x 32 each
+constexpr int kPlainThreads = 256, kPlainTile = 64;
 
 struct GArgs {
   const uint8_t* xq;        // [xrows][K/2]
@@ -32,10 +57,12 @@ struct GArgs {
   int tn;                   // tiles along the output columns
 };
 
+// SEL: byte of the scale operands
+template <int SEL>
 __device__ __forceinline__ floatx4 mfma_fp4(uint4 a, uint4 b, floatx4 c, uint32_t sa, uint32_t sb) {
   const int32x8 av = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
   const int32x8 bv = {(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, c, 4, 4, 0, (int)sa, 0, (int)sb);
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, c, 4, 4, SEL, (int)sa, SEL, (int)sb);
 }
 
 // First rows and row-tile counts of the experts: start[e] = number of row
@@ -51,35 +78,264 @@ __device__ __forceinline__ int rows_of(const GArgs& a, int e, int* first) {
   return max(hi - lo, 0);
 }
 
-template <int TILE>
+template <int TILE, int THREADS>
 __device__ __forceinline__ void tile_starts(const GArgs& a, int* start) {
-  if (threadIdx.x == 0) {
-    int at = 0;
-    for (int e = 0; e < a.E; ++e) {
-      int f;
-      start[e] = at;
-      at += (rows_of(a, e, &f) + TILE - 1) / TILE;
-    }
-    start[a.E] = at;
+  constexpr int PER = kMaxExperts / THREADS;              // experts per thread
+  __shared__ int wsum[THREADS / pq::kWave];
+  const int tid = (int)threadIdx.x, lane = pq::lane_id(), wv = pq::wave_id();
+  int n[PER], sum = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int e = tid * PER + i;
+    int f;
+    n[i] = e < a.E ? (rows_of(a, e, &f) + TILE - 1) / TILE : 0;
+    sum += n[i];
   }
+  int inc = sum;
+#pragma unroll
+  for (int d = 1; d < pq::kWave; d <<= 1) {
+    const int o = __shfl_up(inc, d, pq::kWave);
+    inc += lane >= d ? o : 0;
+  }
+  if (lane == pq::kWave - 1) wsum[wv] = inc;
+  __syncthreads();
+  int at = inc - sum;
+  for (int w = 0; w < wv; ++w) at += wsum[w];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int e = tid * PER + i;
+    if (e <= a.E) start[e] = at;
+    at += n[i];
+  }
+  if (tid == THREADS - 1 && a.E == kMaxExperts) start[kMaxExperts] = at;
   __syncthreads();
 }
 
-// output column of the tile's B row r: plain, or under SiLU*up runs of 16 as
-// gate, up, gate, up; -1 past the matrix
-__device__ __forceinline__ int b_row(const GArgs& a, int tile_n, int r) {
-  if (!a.silu) {
-    const int n = tile_n * BN + r;
-    return n < a.N ? n : -1;
+// The expert whose row tiles hold row tile mt.
+__device__ __forceinline__ int expert_of(const GArgs& a, const int* start, int mt) {
+  int lo = 0, hi = a.E;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (start[mid] <= mt) lo = mid;
+    else hi = mid;
   }
-  const int c = tile_n * (BN / 2) + (r >> 5) * 16 + (r & 15);
-  if (c >= a.R) return -1;
-  return (r & 16) ? c + a.R : c;
+  return lo;
 }
 
-__global__ __launch_bounds__(kThreads) void gemm_mxfp4_kernel(GArgs a) {
+// x row of row r (of n_rows) of the expert whose rows start at `first`; -1 past them
+__device__ __forceinline__ int x_row(const GArgs& a, int first, int n_rows, int r) {
+  if (r >= n_rows) return -1;
+  if (!a.order) return first + r;
+  const int p = a.order[first + r];
+  const int m = p >= 0 ? p / a.top_k : -1;
+  return m < a.xrows ? m : -1;
+}
+
+// Weight row of row r of a WIDTH-wide column tile: plain, or under SiLU*up in
+// runs of RUN as gate, up, gate, up; -1 past the matrix.
+template <int WIDTH, int RUN>
+__device__ __forceinline__ int b_row(const GArgs& a, int tile_n, int r) {
+  if (!a.silu) {
+    const int n = tile_n * WIDTH + r;
+    return n < a.N ? n : -1;
+  }
+  const int c = tile_n * (WIDTH / 2) + r / (2 * RUN) * RUN + r % RUN;
+  if (c >= a.R) return -1;
+  return (r / RUN) & 1 ? c + a.R : c;
+}
+
+// rows behind the last expert's: zeros
+__device__ __forceinline__ void zero_tail(const GArgs& a, int threads) {
+  if (!a.offsets) return;
+  const int end = min(max(a.offsets[a.E], 0), a.P);
+  for (long i = (long)end * a.R + (long)blockIdx.x * threads + threadIdx.x; i < (long)a.P * a.R;
+       i += (long)gridDim.x * threads)
+    a.y[i] = 0;
+}
+
+// ---------------------------------------------------------------------------
+// tiled kernel
+// ---------------------------------------------------------------------------
+template <int BM>
+struct Stage {
+  uint8_t a[BM * kRowBytes];
+  uint8_t b[BN * kRowBytes];
+  uint8_t sa[BM * 8];
+  uint8_t sb[BN * 8];
+};
+
+template <int N>
+__device__ __forceinline__ void wait_loads_barrier() {
+  // this wave's loads but the N youngest have landed, and with the barrier
+  // every wave's; no wave still reads the stage about to be refilled
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+template <int BM, int S>
+__global__ __launch_bounds__(kThreads) void gemm_mxfp4_tiled_kernel(GArgs a) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  Stage<BM>* st = reinterpret_cast<Stage<BM>*>(smem);
   __shared__ int start[kMaxExperts + 1];
-  tile_starts<BM>(a, start);
+  constexpr int WM = BM / 32;                  // 16-row sub-tiles per wave
+  constexpr int LA = BM >= 64 ? BM / 64 : 1;   // A loads of a wave and stage (below 64 rows two waves load the same)
+  constexpr int kLoads = LA + BN / 64 + 2;
+  tile_starts<BM, kThreads>(a, start);
+  const int lane = pq::lane_id();
+  const int wv = __builtin_amdgcn_readfirstlane(pq::wave_id());
+  const int wm = wv >> 2, wn = wv & 3, rl = lane & 15, lg = lane >> 4;
+  const int total = start[a.E] * a.tn;
+  const int nb = a.K / pq::kMxBlock, nk = (nb + 7) / 8;
+  const uint32_t rowb = (uint32_t)(a.K / 2);
+  const pq::int32x4 xr = pq::rsrc_words(a.xq, (uint32_t)((size_t)a.xrows * rowb));
+  const pq::int32x4 xsr = pq::rsrc_words(a.xs, (uint32_t)((size_t)a.xrows * nb));
+  const int G = (int)gridDim.x, b = (int)blockIdx.x;
+  const int slot = G % kXcds == 0 ? (b % kXcds) * (G / kXcds) + b / kXcds : b;   // block b runs on XCD b % 8
+
+  // a load instruction covers 8 rows: lane's row and piece (it lands in slot lane % 8)
+  const int arow_l = BM >= 64 ? 8 * wv + (lane >> 3) : 8 * (wv & 3) + (lane >> 3);
+  const int brow_l = 8 * wv + (lane >> 3);
+  const int piece = (lane & 7) ^ (lane >> 3);
+  // scale loads: 32 rows of two dwords
+  constexpr int kSaWaves = BM / 32;
+  const int sarow = 32 * (wv % kSaWaves) + (lane >> 1), sbrow = 32 * wv + (lane >> 1);
+  const int half = lane & 1;
+
+  for (int i0 = slot; i0 < total; i0 += G) {
+    const int e = __builtin_amdgcn_readfirstlane([&] {
+      int lo = 0, hi = a.E;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if ((long)start[mid] * a.tn <= i0) lo = mid;
+        else hi = mid;
+      }
+      return lo;
+    }());
+    int first;
+    const int n_rows = rows_of(a, e, &first);
+    const int tm = __builtin_amdgcn_readfirstlane(start[e + 1] - start[e]);
+    const int local = i0 - __builtin_amdgcn_readfirstlane(start[e]) * a.tn;
+    const int grp = local / (kGroupM * a.tn);
+    const int gsz = min(kGroupM, tm - grp * kGroupM);
+    const int lg_ = local - grp * kGroupM * a.tn;
+    const int m0 = (grp * kGroupM + lg_ % gsz) * BM, tile_n = lg_ / gsz;
+    const pq::int32x4 wr = pq::rsrc_words(a.w + (size_t)e * a.N * rowb, (uint32_t)((size_t)a.N * rowb));
+    const pq::int32x4 wsr = pq::rsrc_words(a.ws + (size_t)e * a.N * nb, (uint32_t)((size_t)a.N * nb));
+
+    uint32_t aoff[LA], boff[BN / 64], saoff, sboff;
+#pragma unroll
+    for (int i = 0; i < LA; ++i) {
+      const int r = x_row(a, first, n_rows, m0 + 64 * i + arow_l);
+      aoff[i] = r >= 0 ? (uint32_t)r * rowb + 16u * piece : pq::kOOB;
+    }
+#pragma unroll
+    for (int i = 0; i < BN / 64; ++i) {
+      const int r = b_row<BN, 32>(a, tile_n, 64 * i + brow_l);
+      boff[i] = r >= 0 ? (uint32_t)r * rowb + 16u * piece : pq::kOOB;
+    }
+    {
+      const int ra = x_row(a, first, n_rows, m0 + sarow), rb = b_row<BN, 32>(a, tile_n, sbrow);
+      saoff = ra >= 0 ? (uint32_t)ra * nb + 4u * half : pq::kOOB;
+      sboff = rb >= 0 ? (uint32_t)rb * nb + 4u * half : pq::kOOB;
+    }
+
+    // the loads of step k into stage s (zeros past the last step, so that every
+    // step issues the same number); a last step of 4 blocks has no upper half
+    auto issue = [&](int s, int k) {
+      Stage<BM>& t = st[s];
+      const bool live = k < nk;
+      const bool lo_only = 8 * k + 8 > nb;
+      const bool pk = live && (!lo_only || piece < 4), hk = live && (!lo_only || half == 0);
+      const uint32_t kofs = (uint32_t)__builtin_amdgcn_readfirstlane(k * kRowBytes);
+      const uint32_t sofs = (uint32_t)__builtin_amdgcn_readfirstlane(k * 8);
+#pragma unroll
+      for (int i = 0; i < LA; ++i)
+        pq::dma16(xr, pq::lds_addr(t.a + (BM >= 64 ? 64 * i + 8 * wv : 8 * (wv & 3)) * kRowBytes),
+                  pk ? aoff[i] : pq::kOOB, kofs);
+#pragma unroll
+      for (int i = 0; i < BN / 64; ++i)
+        pq::dma16(wr, pq::lds_addr(t.b + (64 * i + 8 * wv) * kRowBytes), pk ? boff[i] : pq::kOOB, kofs);
+      pq::dma4(xsr, pq::lds_addr(t.sa + 256 * (wv % kSaWaves)), hk ? saoff : pq::kOOB, sofs);
+      pq::dma4(wsr, pq::lds_addr(t.sb + 256 * wv), hk ? sboff : pq::kOOB, sofs);
+    };
+
+    floatx4 acc[WM][4];
+#pragma unroll
+    for (int i = 0; i < WM; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][j] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+
+    auto compute = [&](const Stage<BM>& t) {
+      uint4 bf[4][2];
+      uint32_t sbv[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int r = 64 * wn + 16 * j + rl;
+        const uint8_t* p = t.b + r * kRowBytes;
+        bf[j][0] = *reinterpret_cast<const uint4*>(p + 16 * ((2 * lg) ^ (rl & 7)));
+        bf[j][1] = *reinterpret_cast<const uint4*>(p + 16 * ((2 * lg + 1) ^ (rl & 7)));
+        sbv[j] = *reinterpret_cast<const uint16_t*>(t.sb + r * 8 + 2 * lg);
+      }
+#pragma unroll
+      for (int i = 0; i < WM; ++i) {
+        const int r = (BM / 2) * wm + 16 * i + rl;
+        const uint8_t* p = t.a + r * kRowBytes;
+        const uint4 a0 = *reinterpret_cast<const uint4*>(p + 16 * ((2 * lg) ^ (rl & 7)));
+        const uint4 a1 = *reinterpret_cast<const uint4*>(p + 16 * ((2 * lg + 1) ^ (rl & 7)));
+        const uint32_t sav = *reinterpret_cast<const uint16_t*>(t.sa + r * 8 + 2 * lg);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = mfma_fp4<0>(a0, bf[j][0], acc[i][j], sav, sbv[j]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = mfma_fp4<1>(a1, bf[j][1], acc[i][j], sav, sbv[j]);
+      }
+    };
+
+#pragma unroll
+    for (int s = 0; s < S - 1; ++s) issue(s, s);
+    for (int k0 = 0; k0 < nk; k0 += S) {
+#pragma unroll
+      for (int s = 0; s < S; ++s) {
+        if (k0 + s < nk) {
+          wait_loads_barrier<(S - 2) * kLoads>();
+          issue((s + S - 1) % S, k0 + s + S - 1);
+          compute(st[s]);
+        }
+      }
+    }
+    wait_loads_barrier<0>();                   // nothing in flight, and every wave done, before the next tile's loads
+
+    // lane (g, c) of sub-tile (i, j) holds rows 4g .. 4g+3 of i and column c of j
+#pragma unroll
+    for (int i = 0; i < WM; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int row = m0 + (BM / 2) * wm + 16 * i + 4 * lg + r;
+        if (row >= n_rows) continue;
+        uint16_t* yr = a.y + (size_t)(first + row) * a.R;
+        if (a.silu) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int c = tile_n * (BN / 2) + 32 * wn + 16 * j + rl;
+            if (c < a.R) yr[c] = pq::bf16_rne(pq::silu_mul_f32(acc[i][j][r], acc[i][j + 2][r]));
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int n = tile_n * BN + 64 * wn + 16 * j + rl;
+            if (n < a.N) yr[n] = pq::bf16_rne(acc[i][j][r]);
+          }
+        }
+      }
+  }
+  zero_tail(a, kThreads);
+}
+
+// ---------------------------------------------------------------------------
+// plain kernel
+// ---------------------------------------------------------------------------
+__global__ __launch_bounds__(kPlainThreads) void gemm_mxfp4_plain_kernel(GArgs a) {
+  constexpr int BM = kPlainTile, BN = kPlainTile;
+  __shared__ int start[kMaxExperts + 1];
+  tile_starts<BM, kPlainThreads>(a, start);
   const int lane = pq::lane_id(), wv = pq::wave_id();
   const int wm = wv >> 1, wn = wv & 1, rl = lane & 15, g = lane >> 4;
   const int total = start[a.E] * a.tn;
@@ -89,12 +345,7 @@ __global__ __launch_bounds__(kThreads) void gemm_mxfp4_kernel(GArgs a) {
   const pq::rsrc_t xsr = pq::make_rsrc(a.xs, (uint32_t)((size_t)a.xrows * nb));
   for (int t = (int)blockIdx.x; t < total; t += (int)gridDim.x) {
     const int mt = t / a.tn, tile_n = t - mt * a.tn;
-    int lo = 0, hi = a.E;                    // the expert whose row tiles hold mt
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      if (start[mid] <= mt) lo = mid;
-      else hi = mid;
-    }
+    const int lo = expert_of(a, start, mt);
     int first;
     const int n_rows = rows_of(a, lo, &first);
     const int m0 = (mt - start[lo]) * BM;
@@ -103,17 +354,8 @@ __global__ __launch_bounds__(kThreads) void gemm_mxfp4_kernel(GArgs a) {
     int arow[2], brow[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int r = m0 + 32 * wm + 16 * i + rl;
-      arow[i] = -1;
-      if (r < n_rows) {
-        if (a.order) {
-          const int p = a.order[first + r];
-          if (p >= 0 && p / a.top_k < a.xrows) arow[i] = p / a.top_k;
-        } else {
-          arow[i] = first + r;
-        }
-      }
-      brow[i] = b_row(a, tile_n, 32 * wn + 16 * i + rl);
+      arow[i] = x_row(a, first, n_rows, m0 + 32 * wm + 16 * i + rl);
+      brow[i] = b_row<BN, 16>(a, tile_n, 32 * wn + 16 * i + rl);
     }
     floatx4 acc[2][2];
 #pragma unroll
@@ -135,7 +377,7 @@ __global__ __launch_bounds__(kThreads) void gemm_mxfp4_kernel(GArgs a) {
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) acc[i][j] = mfma_fp4(av[i], bv[j], acc[i][j], sa[i], sb[j]);
+        for (int j = 0; j < 2; ++j) acc[i][j] = mfma_fp4<0>(av[i], bv[j], acc[i][j], sa[i], sb[j]);
     }
     // lane (g, c) of sub-tile (i, j) holds rows 4g .. 4g+3 of i and column c of j
 #pragma unroll
@@ -157,13 +399,7 @@ __global__ __launch_bounds__(kThreads) void gemm_mxfp4_kernel(GArgs a) {
         }
       }
   }
-  // rows behind the last expert's: zeros
-  if (a.offsets) {
-    const int end = min(max(a.offsets[a.E], 0), a.P);
-    for (long i = (long)end * a.R + (long)blockIdx.x * kThreads + threadIdx.x; i < (long)a.P * a.R;
-         i += (long)gridDim.x * kThreads)
-      a.y[i] = 0;
-  }
+  zero_tail(a, kPlainThreads);
 }
 
 // Shapes shared by the entry points; E and N, K of one expert's matrix.
@@ -176,16 +412,43 @@ int check_shape(int xrows, int P, int K, int N, int E, int epi) {
   return PQ_OK;
 }
 
+// row tiles whatever the offsets, for tiles of `tile` rows
+long most_row_tiles(const GArgs& a, int tile) {
+  return (long)a.P / tile + (a.E < a.P ? a.E : a.P);
+}
+
+template <int BM, int S>
+int launch_tiled(GArgs& a, int num_cus, hipStream_t stream) {
+  constexpr size_t kLds = S * sizeof(Stage<BM>);
+  static_assert(kLds + (kMaxExperts + 1) * 4 + 256 <= 160 * 1024, "stages must fit LDS");
+  auto kern = gemm_mxfp4_tiled_kernel<BM, S>;
+  static pqhost::KernelAttrOnce attr;
+  PQ_HIP_CHECK(pqhost::set_dynamic_lds_once(attr, (const void*)kern, (int)kLds));
+  a.tn = a.silu ? (a.R + BN / 2 - 1) / (BN / 2) : (a.N + BN - 1) / BN;
+  const long most = most_row_tiles(a, BM) * a.tn;
+  hipLaunchKernelGGL(kern, dim3((unsigned)(most < num_cus ? most : num_cus)), dim3(kThreads), kLds, stream, a);
+  PQ_HIP_CHECK(hipGetLastError());
+  return PQ_OK;
+}
+
 int run(GArgs& a, int epi, hipStream_t stream) {
   pqhost::DeviceInfo dev;
   const int st = pqhost::current_device_info(&dev);
   if (st != PQ_OK) return st;
   a.silu = epi == PQ_EPI_SILU_MUL;
   a.R = a.silu ? a.N / 2 : a.N;
-  a.tn = a.silu ? (a.R + BN / 2 - 1) / (BN / 2) : (a.N + BN - 1) / BN;
-  const long most = ((long)a.P / BM + (a.E < a.P ? a.E : a.P)) * a.tn;   // tiles, whatever the offsets
+  if (a.K % 128 == 0) {
+    const char* f = getenv("PQ_MX_BM");
+    int bm = f ? atoi(f) : 256;
+    if (bm == 256) return launch_tiled<256, 2>(a, dev.num_cus, stream);
+    if (bm == 128) return launch_tiled<128, 3>(a, dev.num_cus, stream);
+    if (bm == 64) return launch_tiled<64, 3>(a, dev.num_cus, stream);
+    return launch_tiled<32, 4>(a, dev.num_cus, stream);
+  }
+  a.tn = a.silu ? (a.R + kPlainTile / 2 - 1) / (kPlainTile / 2) : (a.N + kPlainTile - 1) / kPlainTile;
+  const long most = most_row_tiles(a, kPlainTile) * a.tn;
   const long grid = most < 8L * dev.num_cus ? most : 8L * dev.num_cus;
-  hipLaunchKernelGGL(gemm_mxfp4_kernel, dim3((unsigned)grid), dim3(kThreads), 0, stream, a);
+  hipLaunchKernelGGL(gemm_mxfp4_plain_kernel, dim3((unsigned)grid), dim3(kPlainThreads), 0, stream, a);
   PQ_HIP_CHECK(hipGetLastError());
   return PQ_OK;
 }
