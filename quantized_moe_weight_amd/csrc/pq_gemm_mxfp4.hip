@@ -156,12 +156,14 @@ __device__ __forceinline__ void zero_tail(const GArgs& a, int threads) {
 // ---------------------------------------------------------------------------
 // tiled kernel
 // ---------------------------------------------------------------------------
-template <int BM>
-struct Stage {
-  uint8_t a[BM * kRowBytes];
-  uint8_t b[BN * kRowBytes];
-  uint8_t sa[BM * 8];
-  uint8_t sb[BN * 8];
+// LDS: the stages of each operand side by side, so that the operand reads of
+// every stage are one register plus a constant
+template <int BM, int S>
+struct Stages {
+  uint8_t a[S][BM * kRowBytes];
+  uint8_t b[S][BN * kRowBytes];
+  uint8_t sa[S][BM * 8];
+  uint8_t sb[S][BN * 8];
 };
 
 template <int N>
@@ -174,7 +176,7 @@ __device__ __forceinline__ void wait_loads_barrier() {
 template <int BM, int S>
 __global__ __launch_bounds__(kThreads) void gemm_mxfp4_tiled_kernel(GArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
-  Stage<BM>* st = reinterpret_cast<Stage<BM>*>(smem);
+  Stages<BM, S>& st = *reinterpret_cast<Stages<BM, S>*>(smem);
   __shared__ int start[kMaxExperts + 1];
   constexpr int WM = BM / 32;                  // 16-row sub-tiles per wave
   constexpr int LA = BM >= 64 ? BM / 64 : 1;   // A loads of a wave and stage (below 64 rows two waves load the same)
@@ -199,6 +201,13 @@ __global__ __launch_bounds__(kThreads) void gemm_mxfp4_tiled_kernel(GArgs a) {
   constexpr int kSaWaves = BM / 32;
   const int sarow = 32 * (wv % kSaWaves) + (lane >> 1), sbrow = 32 * wv + (lane >> 1);
   const int half = lane & 1;
+
+  // operand reads of this lane: pieces 2g and 2g + 1 of its rows, and their scale bytes
+  const uint32_t sw0 = 16u * (uint32_t)((2 * lg) ^ (rl & 7)), sw1 = 16u * (uint32_t)((2 * lg + 1) ^ (rl & 7));
+  const int ar = (BM / 2) * wm + rl, br = 64 * wn + rl;
+  const uint8_t *pa0 = st.a[0] + ar * kRowBytes + sw0, *pa1 = st.a[0] + ar * kRowBytes + sw1;
+  const uint8_t *pb0 = st.b[0] + br * kRowBytes + sw0, *pb1 = st.b[0] + br * kRowBytes + sw1;
+  const uint8_t *psa = st.sa[0] + ar * 8 + 2 * lg, *psb = st.sb[0] + br * 8 + 2 * lg;
 
   for (int i0 = slot; i0 < total; i0 += G) {
     const int e = __builtin_amdgcn_readfirstlane([&] {
@@ -241,7 +250,6 @@ __global__ __launch_bounds__(kThreads) void gemm_mxfp4_tiled_kernel(GArgs a) {
     // the loads of step k into stage s (zeros past the last step, so that every
     // step issues the same number); a last step of 4 blocks has no upper half
     auto issue = [&](int s, int k) {
-      Stage<BM>& t = st[s];
       const bool live = k < nk;
       const bool lo_only = 8 * k + 8 > nb;
       const bool pk = live && (!lo_only || piece < 4), hk = live && (!lo_only || half == 0);
@@ -249,13 +257,13 @@ __global__ __launch_bounds__(kThreads) void gemm_mxfp4_tiled_kernel(GArgs a) {
       const uint32_t sofs = (uint32_t)__builtin_amdgcn_readfirstlane(k * 8);
 #pragma unroll
       for (int i = 0; i < LA; ++i)
-        pq::dma16(xr, pq::lds_addr(t.a + (BM >= 64 ? 64 * i + 8 * wv : 8 * (wv & 3)) * kRowBytes),
+        pq::dma16(xr, pq::lds_addr(st.a[s] + (BM >= 64 ? 64 * i + 8 * wv : 8 * (wv & 3)) * kRowBytes),
                   pk ? aoff[i] : pq::kOOB, kofs);
 #pragma unroll
       for (int i = 0; i < BN / 64; ++i)
-        pq::dma16(wr, pq::lds_addr(t.b + (64 * i + 8 * wv) * kRowBytes), pk ? boff[i] : pq::kOOB, kofs);
-      pq::dma4(xsr, pq::lds_addr(t.sa + 256 * (wv % kSaWaves)), hk ? saoff : pq::kOOB, sofs);
-      pq::dma4(wsr, pq::lds_addr(t.sb + 256 * wv), hk ? sboff : pq::kOOB, sofs);
+        pq::dma16(wr, pq::lds_addr(st.b[s] + (64 * i + 8 * wv) * kRowBytes), pk ? boff[i] : pq::kOOB, kofs);
+      pq::dma4(xsr, pq::lds_addr(st.sa[s] + 256 * (wv % kSaWaves)), hk ? saoff : pq::kOOB, sofs);
+      pq::dma4(wsr, pq::lds_addr(st.sb[s] + 256 * wv), hk ? sboff : pq::kOOB, sofs);
     };
 
     floatx4 acc[WM][4];
@@ -264,28 +272,31 @@ __global__ __launch_bounds__(kThreads) void gemm_mxfp4_tiled_kernel(GArgs a) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[i][j] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
 
-    auto compute = [&](const Stage<BM>& t) {
-      uint4 bf[4][2];
-      uint32_t sbv[4];
+    // the A reads of sub-tile i + 1 are issued before the products of sub-tile i
+    auto compute = [&](int s) {
+      const int ab = s * BM * kRowBytes, bb = s * BN * kRowBytes, asb = s * BM * 8, bsb = s * BN * 8;
+      uint4 af[2][2], bf[4][2];
+      uint32_t sav[2], sbv[4];
+      auto load_a = [&](int i, int q) {
+        af[q][0] = *reinterpret_cast<const uint4*>(pa0 + ab + 16 * i * kRowBytes);
+        af[q][1] = *reinterpret_cast<const uint4*>(pa1 + ab + 16 * i * kRowBytes);
+        sav[q] = *reinterpret_cast<const uint16_t*>(psa + asb + 16 * i * 8);
+      };
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int r = 64 * wn + 16 * j + rl;
-        const uint8_t* p = t.b + r * kRowBytes;
-        bf[j][0] = *reinterpret_cast<const uint4*>(p + 16 * ((2 * lg) ^ (rl & 7)));
-        bf[j][1] = *reinterpret_cast<const uint4*>(p + 16 * ((2 * lg + 1) ^ (rl & 7)));
-        sbv[j] = *reinterpret_cast<const uint16_t*>(t.sb + r * 8 + 2 * lg);
+        bf[j][0] = *reinterpret_cast<const uint4*>(pb0 + bb + 16 * j * kRowBytes);
+        bf[j][1] = *reinterpret_cast<const uint4*>(pb1 + bb + 16 * j * kRowBytes);
+        sbv[j] = *reinterpret_cast<const uint16_t*>(psb + bsb + 16 * j * 8);
       }
+      load_a(0, 0);
 #pragma unroll
       for (int i = 0; i < WM; ++i) {
-        const int r = (BM / 2) * wm + 16 * i + rl;
-        const uint8_t* p = t.a + r * kRowBytes;
-        const uint4 a0 = *reinterpret_cast<const uint4*>(p + 16 * ((2 * lg) ^ (rl & 7)));
-        const uint4 a1 = *reinterpret_cast<const uint4*>(p + 16 * ((2 * lg + 1) ^ (rl & 7)));
-        const uint32_t sav = *reinterpret_cast<const uint16_t*>(t.sa + r * 8 + 2 * lg);
+        if (i + 1 < WM) load_a(i + 1, (i + 1) & 1);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = mfma_fp4<0>(a0, bf[j][0], acc[i][j], sav, sbv[j]);
+        for (int j = 0; j < 4; ++j) acc[i][j] = mfma_fp4<0>(af[i & 1][0], bf[j][0], acc[i][j], sav[i & 1], sbv[j]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = mfma_fp4<1>(a1, bf[j][1], acc[i][j], sav, sbv[j]);
+        for (int j = 0; j < 4; ++j) acc[i][j] = mfma_fp4<1>(af[i & 1][1], bf[j][1], acc[i][j], sav[i & 1], sbv[j]);
       }
     };
 
@@ -297,7 +308,7 @@ __global__ __launch_bounds__(kThreads) void gemm_mxfp4_tiled_kernel(GArgs a) {
         if (k0 + s < nk) {
           wait_loads_barrier<(S - 2) * kLoads>();
           issue((s + S - 1) % S, k0 + s + S - 1);
-          compute(st[s]);
+          compute(s);
         }
       }
     }
@@ -419,7 +430,7 @@ long most_row_tiles(const GArgs& a, int tile) {
 
 template <int BM, int S>
 int launch_tiled(GArgs& a, int num_cus, hipStream_t stream) {
-  constexpr size_t kLds = S * sizeof(Stage<BM>);
+  constexpr size_t kLds = sizeof(Stages<BM, S>);
   static_assert(kLds + (kMaxExperts + 1) * 4 + 256 <= 160 * 1024, "stages must fit LDS");
   auto kern = gemm_mxfp4_tiled_kernel<BM, S>;
   static pqhost::KernelAttrOnce attr;
