@@ -415,65 +415,83 @@ class MoeLayerCall:
 # streams and captured graphs never share it.
 # ---------------------------------------------------------------------------
 
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
 def _need_here(t, dtypes, ndim, name):
-    """_need for one of several dtypes, and on the current device, whose stream the call goes to."""
-    if isinstance(t, torch.Tensor) and t.dtype not in dtypes:
+    """Check one tensor's metadata, and that it is on the current device, whose stream the call goes to."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA (HIP) tensor")
+    if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
-    _need(t, t.dtype if isinstance(t, torch.Tensor) else None, ndim, name)
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    if t.dim() != ndim:
+        raise ValueError(f"{name} must have {ndim} dims, got shape {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.get_device() != _current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{_current_device()}")
 
 
-def _out(out, shape, dtype, like, name="out"):
-    """The given output, checked, or a new one."""
+def _stream_here():
+    """The current stream of the current device, as the integer the C calls take."""
+    return _raw_stream(_current_device())
+
+
+def _out(out, shape, dtype, like, **inputs):
+    """A new output, or the given one, checked; it must not overlap the inputs named, which other blocks of the
+    kernel may still read when one writes."""
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
-    _need_here(out, (dtype,), len(shape), name)
+        return like.new_empty(shape, dtype=dtype)
+    _need_here(out, (dtype,), len(shape), "out")
     if tuple(out.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(out.shape)}")
+        raise ValueError(f"out must have shape {tuple(shape)}, got {tuple(out.shape)}")
+    b, e = out.data_ptr(), out.data_ptr() + out.nbytes
+    for name, t in inputs.items():
+        if t.data_ptr() < e and b < t.data_ptr() + t.nbytes:
+            raise ValueError(f"out must not overlap {name}")
     return out
 
 
-def _apart(out, out_name, **inputs):
-    """An output that a kernel writes while others of its blocks still read the inputs must not overlap them."""
-    b, e = out.data_ptr(), out.data_ptr() + out.numel() * out.element_size()
-    for name, t in inputs.items():
-        if t is not None and t.data_ptr() < e and b < t.data_ptr() + t.numel() * t.element_size():
-            raise ValueError(f"{out_name} must not overlap {name}")
-
-
+_U8, _I32, _F32, _BF16 = (torch.uint8,), (torch.int32,), (torch.float32,), (torch.bfloat16,)
 _ROW_TYPES = (torch.bfloat16, torch.float32)
+
+
+def _a(t):
+    """The address of a tensor, as the C calls take it."""
+    return t.data_ptr() if t is not None else None
 
 
 def quantize_mxfp4(t: torch.Tensor):
     """MXFP4 quantisation of bf16 or fp32 rows [R, K] -> (codes uint8 [R, K/2], scale bytes uint8 [R, K/32])."""
     _need_here(t, _ROW_TYPES, 2, "t")
     R, K = t.shape
-    codes = torch.empty((R, K // 2), dtype=torch.uint8, device=t.device)
-    scales = torch.empty((R, max(K // 32, 1)), dtype=torch.uint8, device=t.device)
-    _check(lib().pq_quantize_mxfp4(_p(t), int(t.dtype == torch.float32), R, K, _p(codes), _p(scales), _stream()),
+    codes = t.new_empty((R, K // 2), dtype=torch.uint8)
+    scales = t.new_empty((R, max(K // 32, 1)), dtype=torch.uint8)
+    _check(_lib.load().pq_quantize_mxfp4(_a(t), int(t.dtype == torch.float32), R, K, _a(codes), _a(scales), _stream_here()),
            "pq_quantize_mxfp4")
     return codes, scales
 
 
 def dequantize_mxfp4(codes, scales, dtype=torch.bfloat16, out=None):
     """The values [R, K] (bf16 or fp32) of MXFP4 codes uint8 [R, K/2] and scale bytes uint8 [R, K/32]."""
-    _need_here(codes, (torch.uint8,), 2, "codes")
-    _need_here(scales, (torch.uint8,), 2, "scales")
+    _need_here(codes, _U8, 2, "codes")
+    _need_here(scales, _U8, 2, "scales")
     if dtype not in _ROW_TYPES:
         raise TypeError("dequantize_mxfp4 gives bf16 or fp32")
     R, K = codes.shape[0], codes.shape[1] * 2
     if tuple(scales.shape) != (R, K // 32):
         raise ValueError("code / scale shapes do not match")
-    y = _out(out, (R, K), dtype, codes)
-    _check(lib().pq_dequantize_mxfp4(_p(codes), _p(scales), R, K, int(dtype == torch.float32), _p(y), _stream()),
+    y = _out(out, (R, K), dtype, codes, codes=codes, scales=scales)
+    _check(_lib.load().pq_dequantize_mxfp4(_a(codes), _a(scales), R, K, int(dtype == torch.float32), _a(y), _stream_here()),
            "pq_dequantize_mxfp4")
     return y
 
 
 def _mx_weights(w, w_scale, K, ndim):
-    _need_here(w, (torch.uint8,), ndim, "w")
-    _need_here(w_scale, (torch.uint8,), ndim, "w_scale")
+    _need_here(w, _U8, ndim, "w")
+    _need_here(w_scale, _U8, ndim, "w_scale")
     if w.shape[-1] * 2 != K or w_scale.shape[:-1] != w.shape[:-1] or w_scale.shape[-1] * 32 != K:
         raise ValueError("weight / scale shapes do not match x")
     return w.shape[-2]
@@ -482,33 +500,31 @@ def _mx_weights(w, w_scale, K, ndim):
 def gemv_mxfp4(x, w, w_scale, epi: int = EPI_NONE, out=None):
     """y = epi(x @ w^T) for few tokens: x bf16 [M,K] as it is, M <= 16, w MXFP4 codes [N,K/2] and scale bytes
     [N,K/32].  Returns y (bf16 [M,N] or [M,N/2])."""
-    _need_here(x, (torch.bfloat16,), 2, "x")
+    _need_here(x, _BF16, 2, "x")
     M, K = x.shape
     N = _mx_weights(w, w_scale, K, 2)
-    y = _out(out, (M, N // 2 if epi == EPI_SILU_MUL else N), torch.bfloat16, x)
-    _apart(y, "out", x=x, w=w, w_scale=w_scale)
-    _check(lib().pq_gemv_mxfp4(_p(x), M, K, _p(w), _p(w_scale), N, epi, _p(y), _stream()), "pq_gemv_mxfp4")
+    y = _out(out, (M, N // 2 if epi == EPI_SILU_MUL else N), torch.bfloat16, x, x=x, w=w, w_scale=w_scale)
+    _check(_lib.load().pq_gemv_mxfp4(_a(x), M, K, _a(w), _a(w_scale), N, epi, _a(y), _stream_here()), "pq_gemv_mxfp4")
     return y
 
 
 def gemm_mxfp4(x, w, w_scale, epi: int = EPI_NONE, out=None):
     """y = epi(q(x) @ w^T) on the matrix cores: x bf16 [M,K], quantised live to MXFP4, w codes [N,K/2] and scale
     bytes [N,K/32].  Returns y (bf16 [M,N] or [M,N/2])."""
-    _need_here(x, (torch.bfloat16,), 2, "x")
+    _need_here(x, _BF16, 2, "x")
     M, K = x.shape
     N = _mx_weights(w, w_scale, K, 2)
-    y = _out(out, (M, N // 2 if epi == EPI_SILU_MUL else N), torch.bfloat16, x)
-    _apart(y, "out", w=w, w_scale=w_scale)
-    wsn = int(lib().pq_gemm_mxfp4_workspace(M, K, N, epi))
-    ws = torch.empty(wsn, dtype=torch.uint8, device=x.device)
-    _check(lib().pq_gemm_mxfp4(_p(x), M, K, _p(w), _p(w_scale), N, epi, _p(y), _p(ws), wsn, _stream()),
+    y = _out(out, (M, N // 2 if epi == EPI_SILU_MUL else N), torch.bfloat16, x, w=w, w_scale=w_scale)
+    wsn = int(_lib.load().pq_gemm_mxfp4_workspace(M, K, N, epi))
+    ws = x.new_empty(wsn, dtype=torch.uint8)
+    _check(_lib.load().pq_gemm_mxfp4(_a(x), M, K, _a(w), _a(w_scale), N, epi, _a(y), _a(ws), wsn, _stream_here()),
            "pq_gemm_mxfp4")
     return y
 
 
 def _mx_rows(xq, xs):
-    _need_here(xq, (torch.uint8,), 2, "xq")
-    _need_here(xs, (torch.uint8,), 2, "xs")
+    _need_here(xq, _U8, 2, "xq")
+    _need_here(xs, _U8, 2, "xs")
     rows, K = xq.shape[0], xq.shape[1] * 2
     if tuple(xs.shape) != (rows, K // 32):
         raise ValueError("xq / xs shapes do not match")
@@ -519,9 +535,8 @@ def gemm_mxfp4_prequant(xq, xs, w, w_scale, epi: int = EPI_NONE, out=None):
     """The GEMM of gemm_mxfp4 on an activation that quantize_mxfp4 made (xq [M,K/2], xs [M,K/32])."""
     M, K = _mx_rows(xq, xs)
     N = _mx_weights(w, w_scale, K, 2)
-    y = _out(out, (M, N // 2 if epi == EPI_SILU_MUL else N), torch.bfloat16, xq)
-    _apart(y, "out", xq=xq, xs=xs, w=w, w_scale=w_scale)
-    _check(lib().pq_gemm_mxfp4_prequant(_p(xq), _p(xs), M, K, _p(w), _p(w_scale), N, epi, _p(y), _stream()),
+    y = _out(out, (M, N // 2 if epi == EPI_SILU_MUL else N), torch.bfloat16, xq, xq=xq, xs=xs, w=w, w_scale=w_scale)
+    _check(_lib.load().pq_gemm_mxfp4_prequant(_a(xq), _a(xs), M, K, _a(w), _a(w_scale), N, epi, _a(y), _stream_here()),
            "pq_gemm_mxfp4_prequant")
     return y
 
@@ -534,29 +549,26 @@ class MoePlan(NamedTuple):
 
 
 def _plan(plan, need_offsets=False):
-    _need_here(plan.inverse, (torch.int32,), 2, "plan.inverse")
-    _need_here(plan.order, (torch.int32,), 1, "plan.order")
+    _need_here(plan.inverse, _I32, 2, "plan.inverse")
+    _need_here(plan.order, _I32, 1, "plan.order")
     M, k = plan.inverse.shape
     if plan.order.shape[0] != M * k:
         raise ValueError("plan.order must have one entry per pair of plan.inverse")
     if need_offsets:
-        _need_here(plan.offsets, (torch.int32,), 1, "plan.offsets")
+        _need_here(plan.offsets, _I32, 1, "plan.offsets")
     return M, k
 
 
 def moe_sort(topk_ids, E: int) -> MoePlan:
     """Sort the (token, slot) pairs of topk_ids int32 [M, top_k] by expert, pairs of one expert in pair order.
     An id outside [0, E) stands for no expert (a padded token)."""
-    _need_here(topk_ids, (torch.int32,), 2, "topk_ids")
+    _need_here(topk_ids, _I32, 2, "topk_ids")
     M, k = topk_ids.shape
-    dev = topk_ids.device
-    plan = MoePlan(torch.empty(M * k, dtype=torch.int32, device=dev),
-                   torch.empty((M, k), dtype=torch.int32, device=dev),
-                   torch.empty(max(int(E), 0) + 1, dtype=torch.int32, device=dev))
-    wsn = int(lib().pq_moe_sort_workspace(M, k, E))
-    ws = torch.empty(wsn, dtype=torch.uint8, device=dev) if wsn else None
-    _check(lib().pq_moe_sort(_p(topk_ids), M, k, E, _p(plan.order), _p(plan.inverse), _p(plan.offsets), _p(ws), wsn,
-                             _stream()), "pq_moe_sort")
+    plan = MoePlan(topk_ids.new_empty(M * k), topk_ids.new_empty((M, k)), topk_ids.new_empty(max(int(E), 0) + 1))
+    wsn = int(_lib.load().pq_moe_sort_workspace(M, k, E))
+    ws = topk_ids.new_empty(wsn, dtype=torch.uint8) if wsn else None
+    _check(_lib.load().pq_moe_sort(_a(topk_ids), M, k, E, _a(plan.order), _a(plan.inverse), _a(plan.offsets), _a(ws), wsn,
+                             _stream_here()), "pq_moe_sort")
     return plan
 
 
@@ -567,10 +579,9 @@ def moe_dispatch(x, plan: MoePlan, out=None):
     M, k = _plan(plan)
     if x.shape[0] != M:
         raise ValueError("x must have one row per token of the plan")
-    xs = _out(out, (M * k, x.shape[1]), x.dtype, x)
-    _apart(xs, "out", x=x)
-    _check(lib().pq_moe_dispatch(_p(x), int(x.dtype == torch.float32), M, x.shape[1], k, _p(plan.order),
-                                 _p(plan.inverse), _p(xs), _stream()), "pq_moe_dispatch")
+    xs = _out(out, (M * k, x.shape[1]), x.dtype, x, x=x)
+    _check(_lib.load().pq_moe_dispatch(_a(x), int(x.dtype == torch.float32), M, x.shape[1], k, _a(plan.order),
+                                 _a(plan.inverse), _a(xs), _stream_here()), "pq_moe_dispatch")
     return xs
 
 
@@ -582,13 +593,12 @@ def moe_combine(ys, plan: MoePlan, topk_w=None, out=None):
     if ys.shape[0] != M * k:
         raise ValueError("ys must have one row per pair of the plan")
     if topk_w is not None:
-        _need_here(topk_w, (torch.float32,), 2, "topk_w")
+        _need_here(topk_w, _F32, 2, "topk_w")
         if topk_w.shape != plan.inverse.shape:
             raise ValueError("topk_w must have the plan's shape [M, top_k]")
-    y = _out(out, (M, ys.shape[1]), ys.dtype, ys)
-    _apart(y, "out", ys=ys)
-    _check(lib().pq_moe_combine(_p(ys), int(ys.dtype == torch.float32), M, ys.shape[1], k, _p(plan.inverse),
-                                _p(topk_w), _p(y), _stream()), "pq_moe_combine")
+    y = _out(out, (M, ys.shape[1]), ys.dtype, ys, ys=ys)
+    _check(_lib.load().pq_moe_combine(_a(ys), int(ys.dtype == torch.float32), M, ys.shape[1], k, _a(plan.inverse),
+                                _a(topk_w), _a(y), _stream_here()), "pq_moe_combine")
     return y
 
 
@@ -602,16 +612,15 @@ def moe_combine_grad(dy, ys, plan: MoePlan, topk_w, out=None):
     [M,top_k], 0 for a pair without an expert)."""
     _need_here(dy, _ROW_TYPES, 2, "dy")
     _need_here(ys, (dy.dtype,), 2, "ys")
-    _need_here(topk_w, (torch.float32,), 2, "topk_w")
+    _need_here(topk_w, _F32, 2, "topk_w")
     M, k = _plan(plan)
     H = dy.shape[1]
     if dy.shape[0] != M or tuple(ys.shape) != (M * k, H) or topk_w.shape != plan.inverse.shape:
         raise ValueError("dy, ys and topk_w must have the plan's tokens and pairs")
-    dys = _out(out, (M * k, H), ys.dtype, ys)
-    _apart(dys, "out", dy=dy, ys=ys)
-    dw = torch.empty((M, k), dtype=torch.float32, device=dy.device)
-    _check(lib().pq_moe_combine_grad(_p(dy), _p(ys), int(dy.dtype == torch.float32), M, H, k, _p(plan.order),
-                                     _p(plan.inverse), _p(topk_w), _p(dys), _p(dw), _stream()), "pq_moe_combine_grad")
+    dys = _out(out, (M * k, H), ys.dtype, ys, dy=dy, ys=ys)
+    dw = topk_w.new_empty((M, k))
+    _check(_lib.load().pq_moe_combine_grad(_a(dy), _a(ys), int(dy.dtype == torch.float32), M, H, k, _a(plan.order),
+                                     _a(plan.inverse), _a(topk_w), _a(dys), _a(dw), _stream_here()), "pq_moe_combine_grad")
     return dys, dw
 
 
@@ -632,15 +641,14 @@ def gemm_mxfp4_grouped(x, w, w_scale, plan: MoePlan, epi: int = EPI_NONE, gather
     gather: x bf16 [M,K] holds the tokens (src = plan.order[r] // top_k), else [P,K] the sorted rows (src = r).
     w MXFP4 codes [E,N,K/2], w_scale bytes [E,N,K/32].  Returns y bf16 [P,N] (or [P,N/2]); rows without a pair are
     zeros."""
-    _need_here(x, (torch.bfloat16,), 2, "x")
+    _need_here(x, _BF16, 2, "x")
     rows, K = x.shape
     N, E, k, P = _grouped_args(rows, K, w, w_scale, plan, gather)
-    y = _out(out, (P, N // 2 if epi == EPI_SILU_MUL else N), torch.bfloat16, x)
-    _apart(y, "out", w=w, w_scale=w_scale)
-    wsn = int(lib().pq_gemm_mxfp4_grouped_workspace(rows, K, N, epi))
-    ws = torch.empty(wsn, dtype=torch.uint8, device=x.device)
-    _check(lib().pq_gemm_mxfp4_grouped(_p(x), rows, K, _p(plan.order if gather else None), k, _p(plan.offsets), P, E,
-                                       _p(w), _p(w_scale), N, epi, _p(y), _p(ws), wsn, _stream()),
+    y = _out(out, (P, N // 2 if epi == EPI_SILU_MUL else N), torch.bfloat16, x, w=w, w_scale=w_scale)
+    wsn = int(_lib.load().pq_gemm_mxfp4_grouped_workspace(rows, K, N, epi))
+    ws = x.new_empty(wsn, dtype=torch.uint8)
+    _check(_lib.load().pq_gemm_mxfp4_grouped(_a(x), rows, K, _a(plan.order if gather else None), k, _a(plan.offsets), P, E,
+                                       _a(w), _a(w_scale), N, epi, _a(y), _a(ws), wsn, _stream_here()),
            "pq_gemm_mxfp4_grouped")
     return y
 
@@ -650,10 +658,9 @@ def gemm_mxfp4_grouped_prequant(xq, xs, w, w_scale, plan: MoePlan, epi: int = EP
     """The products of gemm_mxfp4_grouped on rows that quantize_mxfp4 made (xq [rows,K/2], xs [rows,K/32])."""
     rows, K = _mx_rows(xq, xs)
     N, E, k, P = _grouped_args(rows, K, w, w_scale, plan, gather)
-    y = _out(out, (P, N // 2 if epi == EPI_SILU_MUL else N), torch.bfloat16, xq)
-    _apart(y, "out", xq=xq, xs=xs, w=w, w_scale=w_scale)
-    _check(lib().pq_gemm_mxfp4_grouped_prequant(_p(xq), _p(xs), rows, K, _p(plan.order if gather else None), k,
-                                                _p(plan.offsets), P, E, _p(w), _p(w_scale), N, epi, _p(y), _stream()),
+    y = _out(out, (P, N // 2 if epi == EPI_SILU_MUL else N), torch.bfloat16, xq, xq=xq, xs=xs, w=w, w_scale=w_scale)
+    _check(_lib.load().pq_gemm_mxfp4_grouped_prequant(_a(xq), _a(xs), rows, K, _a(plan.order if gather else None), k,
+                                                _a(plan.offsets), P, E, _a(w), _a(w_scale), N, epi, _a(y), _stream_here()),
            "pq_gemm_mxfp4_grouped_prequant")
     return y
 
@@ -665,7 +672,7 @@ def moe_prefill_layer_mxfp4(x, w13, s13, w2, s2, topk_ids, topk_w, out=None):
     x bf16 [M,H]; w13 codes [E,2I,H/2], s13 bytes [E,2I,H/32] (gate rows, then up rows); w2 codes [E,H,I/2], s2 bytes
     [E,H,I/32]; topk_ids int32 [M,top_k] (outside [0,E): no expert), topk_w fp32 [M,top_k].  Both products quantise
     their input live, as moe_decode_layer does.  Returns y bf16 [M,H]."""
-    _need_here(w13, (torch.uint8,), 3, "w13")
+    _need_here(w13, _U8, 3, "w13")
     plan = moe_sort(topk_ids, w13.shape[0])
     h = gemm_mxfp4_grouped(x, w13, s13, plan, EPI_SILU_MUL)
     return moe_combine(gemm_mxfp4_grouped(h, w2, s2, plan, gather=False), plan, topk_w, out)

@@ -201,6 +201,6 @@ def test_refusals(pq, monkeypatch):
         pq.moe_combine_grad(x, ys.to(torch.bfloat16), plan, w)
     with pytest.raises(ValueError):
         pq.moe_combine_grad(x, ys, plan, w, out=torch.zeros((8, 8), device="cuda"))
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    monkeypatch.setattr(pq, "_current_device", lambda: 1)
     with pytest.raises(ValueError):
         pq.moe_sort(ids, 4)

@@ -401,6 +401,6 @@ def test_refusals(pq, monkeypatch):
         pq.gemm_mxfp4_grouped(x, wg[:2].contiguous(), sg[:2].contiguous(), plan)
     with pytest.raises(ValueError):
         pq.gemm_mxfp4_grouped(x, wg, sg, plan, gather=False)
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    monkeypatch.setattr(pq, "_current_device", lambda: 1)
     with pytest.raises(ValueError):                 # a tensor of another device than the current one
         pq.gemv_mxfp4(x, w, s)
