@@ -157,30 +157,56 @@ __device__ __forceinline__ void zero_tail(const GArgs& a, int threads) {
 // tiled kernel
 // ---------------------------------------------------------------------------
 // LDS: the stages of each operand side by side, so that the operand reads of
-// every stage are one register plus a constant
+// every stage are one register plus a constant.  A scale buffer holds two
+// steps (16 bytes of a row): a row's scale line is then read from L2 half as
+// often as with one step a time (the L1 does not hold it that long).
 template <int BM, int S>
 struct Stages {
   uint8_t a[S][BM * kRowBytes];
   uint8_t b[S][BN * kRowBytes];
-  uint8_t sa[S][BM * 8];
-  uint8_t sb[S][BN * 8];
+  uint8_t sa[2][BM * 16];
+  uint8_t sb[2][BN * 16];
 };
 
 template <int N>
 __device__ __forceinline__ void wait_loads_barrier() {
-  // this wave's loads but the N youngest have landed, and with the barrier
-  // every wave's; no wave still reads the stage about to be refilled
+  // at most N of this wave's loads are outstanding, its LDS reads are done,
+  // and with the barrier every wave's
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+// A tile of the persistent loop, wave-uniform.
+struct Tile {
+  int e, first, n_rows, m0, tile_n;
+};
+
+// Tile i of the order: experts one after the other; within an expert groups of
+// kGroupM row tiles, a group's row tiles before its next column tile.
+template <int BM>
+__device__ __forceinline__ Tile tile_at(const GArgs& a, const int* start, int i) {
+  Tile t;
+  t.e = __builtin_amdgcn_readfirstlane(expert_of(a, start, i / a.tn));
+  const int st = __builtin_amdgcn_readfirstlane(start[t.e]);
+  const int tm = __builtin_amdgcn_readfirstlane(start[t.e + 1]) - st;
+  t.n_rows = __builtin_amdgcn_readfirstlane(rows_of(a, t.e, &t.first));
+  t.first = __builtin_amdgcn_readfirstlane(t.first);
+  const int local = i - st * a.tn;
+  const int grp = local / (kGroupM * a.tn);
+  const int gsz = min(kGroupM, tm - grp * kGroupM);
+  const int in = local - grp * kGroupM * a.tn;
+  t.m0 = (grp * kGroupM + in % gsz) * BM;
+  t.tile_n = in / gsz;
+  return t;
 }
 
 template <int BM, int S>
 __global__ __launch_bounds__(kThreads) void gemm_mxfp4_tiled_kernel(GArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   Stages<BM, S>& st = *reinterpret_cast<Stages<BM, S>*>(smem);
-  __shared__ int start[kMaxExperts + 1];
+  int* start = reinterpret_cast<int*>(smem + sizeof(Stages<BM, S>));   // [E + 1]
   constexpr int WM = BM / 32;                  // 16-row sub-tiles per wave
-  constexpr int LA = BM >= 64 ? BM / 64 : 1;   // A loads of a wave and stage (below 64 rows two waves load the same)
-  constexpr int kLoads = LA + BN / 64 + 2;
+  constexpr int LA = BM / 64;                  // A loads of a wave and stage
+  constexpr int kLoads = LA + BN / 64;         // code loads of a wave and stage
   tile_starts<BM, kThreads>(a, start);
   const int lane = pq::lane_id();
   const int wv = __builtin_amdgcn_readfirstlane(pq::wave_id());
@@ -194,148 +220,170 @@ __global__ __launch_bounds__(kThreads) void gemm_mxfp4_tiled_kernel(GArgs a) {
   const int slot = G % kXcds == 0 ? (b % kXcds) * (G / kXcds) + b / kXcds : b;   // block b runs on XCD b % 8
 
   // a load instruction covers 8 rows: lane's row and piece (it lands in slot lane % 8)
-  const int arow_l = BM >= 64 ? 8 * wv + (lane >> 3) : 8 * (wv & 3) + (lane >> 3);
-  const int brow_l = 8 * wv + (lane >> 3);
+  const int row_l = 8 * wv + (lane >> 3);
   const int piece = (lane & 7) ^ (lane >> 3);
-  // scale loads: 32 rows of two dwords
-  constexpr int kSaWaves = BM / 32;
-  const int sarow = 32 * (wv % kSaWaves) + (lane >> 1), sbrow = 32 * wv + (lane >> 1);
-  const int half = lane & 1;
+  // scales: a whole wave loads 64 rows of A (waves below BM / 64) or of B
+  const bool s_a = wv < LA;
+  const int srow = 64 * (s_a ? wv : wv - LA) + lane;
 
   // operand reads of this lane: pieces 2g and 2g + 1 of its rows, and their scale bytes
   const uint32_t sw0 = 16u * (uint32_t)((2 * lg) ^ (rl & 7)), sw1 = 16u * (uint32_t)((2 * lg + 1) ^ (rl & 7));
   const int ar = (BM / 2) * wm + rl, br = 64 * wn + rl;
   const uint8_t *pa0 = st.a[0] + ar * kRowBytes + sw0, *pa1 = st.a[0] + ar * kRowBytes + sw1;
   const uint8_t *pb0 = st.b[0] + br * kRowBytes + sw0, *pb1 = st.b[0] + br * kRowBytes + sw1;
-  const uint8_t *psa = st.sa[0] + ar * 8 + 2 * lg, *psb = st.sb[0] + br * 8 + 2 * lg;
+  const uint8_t *psa = st.sa[0] + ar * 16 + 2 * lg, *psb = st.sb[0] + br * 16 + 2 * lg;
 
-  for (int i0 = slot; i0 < total; i0 += G) {
-    const int e = __builtin_amdgcn_readfirstlane([&] {
-      int lo = 0, hi = a.E;
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if ((long)start[mid] * a.tn <= i0) lo = mid;
-        else hi = mid;
-      }
-      return lo;
-    }());
-    int first;
-    const int n_rows = rows_of(a, e, &first);
-    const int tm = __builtin_amdgcn_readfirstlane(start[e + 1] - start[e]);
-    const int local = i0 - __builtin_amdgcn_readfirstlane(start[e]) * a.tn;
-    const int grp = local / (kGroupM * a.tn);
-    const int gsz = min(kGroupM, tm - grp * kGroupM);
-    const int lg_ = local - grp * kGroupM * a.tn;
-    const int m0 = (grp * kGroupM + lg_ % gsz) * BM, tile_n = lg_ / gsz;
-    const pq::int32x4 wr = pq::rsrc_words(a.w + (size_t)e * a.N * rowb, (uint32_t)((size_t)a.N * rowb));
-    const pq::int32x4 wsr = pq::rsrc_words(a.ws + (size_t)e * a.N * nb, (uint32_t)((size_t)a.N * nb));
-
-    uint32_t aoff[LA], boff[BN / 64], saoff, sboff;
+  uint32_t aoff[LA], boff[BN / 64], soff;
+  pq::int32x4 wr, wsr;
+  auto aim = [&](const Tile& t) {
+    wr = pq::rsrc_words(a.w + (size_t)t.e * a.N * rowb, (uint32_t)((size_t)a.N * rowb));
+    wsr = pq::rsrc_words(a.ws + (size_t)t.e * a.N * nb, (uint32_t)((size_t)a.N * nb));
 #pragma unroll
     for (int i = 0; i < LA; ++i) {
-      const int r = x_row(a, first, n_rows, m0 + 64 * i + arow_l);
+      const int r = x_row(a, t.first, t.n_rows, t.m0 + 64 * i + row_l);
       aoff[i] = r >= 0 ? (uint32_t)r * rowb + 16u * piece : pq::kOOB;
     }
 #pragma unroll
     for (int i = 0; i < BN / 64; ++i) {
-      const int r = b_row<BN, 32>(a, tile_n, 64 * i + brow_l);
+      const int r = b_row<BN, 32>(a, t.tile_n, 64 * i + row_l);
       boff[i] = r >= 0 ? (uint32_t)r * rowb + 16u * piece : pq::kOOB;
     }
-    {
-      const int ra = x_row(a, first, n_rows, m0 + sarow), rb = b_row<BN, 32>(a, tile_n, sbrow);
-      saoff = ra >= 0 ? (uint32_t)ra * nb + 4u * half : pq::kOOB;
-      sboff = rb >= 0 ? (uint32_t)rb * nb + 4u * half : pq::kOOB;
+    const int r = wv >= LA + BN / 64 ? -1 : s_a ? x_row(a, t.first, t.n_rows, t.m0 + srow) : b_row<BN, 32>(a, t.tile_n, srow);
+    soff = r >= 0 ? (uint32_t)r * nb : pq::kOOB;
+  };
+
+  // the loads of step k into stage s (zeros past the last step, so that every
+  // step issues the same number); a last step of 4 blocks has no upper half
+  auto issue = [&](int s, int k) {
+    const bool ok = k < nk && (8 * k + 8 <= nb || piece < 4);
+    const uint32_t kofs = (uint32_t)__builtin_amdgcn_readfirstlane(k * kRowBytes);
+#pragma unroll
+    for (int i = 0; i < LA; ++i)
+      pq::dma16(xr, pq::lds_addr(st.a[s] + (64 * i + 8 * wv) * kRowBytes), ok ? aoff[i] : pq::kOOB, kofs);
+#pragma unroll
+    for (int i = 0; i < BN / 64; ++i)
+      pq::dma16(wr, pq::lds_addr(st.b[s] + (64 * i + 8 * wv) * kRowBytes), ok ? boff[i] : pq::kOOB, kofs);
+  };
+  // the scales of steps 2p and 2p + 1 into buffer p % 2: 16 bytes a row, the
+  // last ones as dwords, with zeros past K (a zero code times another row's NaN
+  // scale would be NaN)
+  auto issue_scales = [&](int p) {
+    if (16 * p >= nb || wv >= LA + BN / 64) return;
+    uint8_t* to = s_a ? st.sa[p & 1] + wv * 1024 : st.sb[p & 1] + (wv - LA) * 1024;
+    const pq::int32x4 r = {s_a ? xsr[0] : wsr[0], s_a ? xsr[1] : wsr[1], s_a ? xsr[2] : wsr[2], 0x00020000};
+    const uint32_t pofs = (uint32_t)__builtin_amdgcn_readfirstlane(16 * p);
+    if (16 * p + 16 <= nb) {
+      pq::dma16(r, pq::lds_addr(to), soff, pofs);
+    } else {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t o = (uint32_t)__shfl((int)soff, 16 * q + (lane >> 2), pq::kWave);
+        pq::dma4(r, pq::lds_addr(to + 256 * q), 16 * p + 4 * (lane & 3) < nb ? o + 4u * (lane & 3) : pq::kOOB, pofs);
+      }
     }
+  };
+  // everything that step k adds to what is in flight
+  auto feed = [&](int s, int k) {
+    if (k >= nk) return;
+    if (k % 2 == 0) issue_scales(k / 2);
+    issue(s, k);
+  };
 
-    // the loads of step k into stage s (zeros past the last step, so that every
-    // step issues the same number); a last step of 4 blocks has no upper half
-    auto issue = [&](int s, int k) {
-      const bool live = k < nk;
-      const bool lo_only = 8 * k + 8 > nb;
-      const bool pk = live && (!lo_only || piece < 4), hk = live && (!lo_only || half == 0);
-      const uint32_t kofs = (uint32_t)__builtin_amdgcn_readfirstlane(k * kRowBytes);
-      const uint32_t sofs = (uint32_t)__builtin_amdgcn_readfirstlane(k * 8);
-#pragma unroll
-      for (int i = 0; i < LA; ++i)
-        pq::dma16(xr, pq::lds_addr(st.a[s] + (BM >= 64 ? 64 * i + 8 * wv : 8 * (wv & 3)) * kRowBytes),
-                  pk ? aoff[i] : pq::kOOB, kofs);
-#pragma unroll
-      for (int i = 0; i < BN / 64; ++i)
-        pq::dma16(wr, pq::lds_addr(st.b[s] + (64 * i + 8 * wv) * kRowBytes), pk ? boff[i] : pq::kOOB, kofs);
-      pq::dma4(xsr, pq::lds_addr(st.sa[s] + 256 * (wv % kSaWaves)), hk ? saoff : pq::kOOB, sofs);
-      pq::dma4(wsr, pq::lds_addr(st.sb[s] + 256 * wv), hk ? sboff : pq::kOOB, sofs);
+  floatx4 acc[WM][4];
+  // the A reads of sub-tile i + 1 are issued before the products of sub-tile i.
+  // The weights are the first operand: a lane then holds four consecutive
+  // outputs of one row
+  auto compute = [&](int s, int buf, int odd) {
+    const int ab = s * BM * kRowBytes, bb = s * BN * kRowBytes;
+    const uint8_t *qa = psa + buf * BM * 16 + 8 * odd, *qb = psb + buf * BN * 16 + 8 * odd;
+    uint4 af[2][2], bf[4][2];
+    uint32_t sav[2], sbv[4];
+    auto load_a = [&](int i, int q) {
+      af[q][0] = *reinterpret_cast<const uint4*>(pa0 + ab + 16 * i * kRowBytes);
+      af[q][1] = *reinterpret_cast<const uint4*>(pa1 + ab + 16 * i * kRowBytes);
+      sav[q] = *reinterpret_cast<const uint16_t*>(qa + 16 * i * 16);
     };
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      bf[j][0] = *reinterpret_cast<const uint4*>(pb0 + bb + 16 * j * kRowBytes);
+      bf[j][1] = *reinterpret_cast<const uint4*>(pb1 + bb + 16 * j * kRowBytes);
+      sbv[j] = *reinterpret_cast<const uint16_t*>(qb + 16 * j * 16);
+    }
+    load_a(0, 0);
+#pragma unroll
+    for (int i = 0; i < WM; ++i) {
+      if (i + 1 < WM) load_a(i + 1, (i + 1) & 1);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][j] = mfma_fp4<0>(bf[j][0], af[i & 1][0], acc[i][j], sbv[j], sav[i & 1]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][j] = mfma_fp4<1>(bf[j][1], af[i & 1][1], acc[i][j], sbv[j], sav[i & 1]);
+    }
+  };
 
-    floatx4 acc[WM][4];
+  Tile t = {};
+  if (slot < total) {
+    t = tile_at<BM>(a, start, slot);
+    aim(t);
+#pragma unroll
+    for (int s = 0; s < S - 1; ++s) feed(s, s);
+  }
+  for (int i0 = slot; i0 < total; i0 += G) {
 #pragma unroll
     for (int i = 0; i < WM; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[i][j] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
-
-    // the A reads of sub-tile i + 1 are issued before the products of sub-tile i
-    auto compute = [&](int s) {
-      const int ab = s * BM * kRowBytes, bb = s * BN * kRowBytes, asb = s * BM * 8, bsb = s * BN * 8;
-      uint4 af[2][2], bf[4][2];
-      uint32_t sav[2], sbv[4];
-      auto load_a = [&](int i, int q) {
-        af[q][0] = *reinterpret_cast<const uint4*>(pa0 + ab + 16 * i * kRowBytes);
-        af[q][1] = *reinterpret_cast<const uint4*>(pa1 + ab + 16 * i * kRowBytes);
-        sav[q] = *reinterpret_cast<const uint16_t*>(psa + asb + 16 * i * 8);
-      };
+    // unrolled over the stages and the two steps of a scale buffer
+    constexpr int U = S % 2 == 0 ? 2 * S : 4 * S;
+    for (int k0 = 0; k0 < nk; k0 += U) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        bf[j][0] = *reinterpret_cast<const uint4*>(pb0 + bb + 16 * j * kRowBytes);
-        bf[j][1] = *reinterpret_cast<const uint4*>(pb1 + bb + 16 * j * kRowBytes);
-        sbv[j] = *reinterpret_cast<const uint16_t*>(psb + bsb + 16 * j * 8);
-      }
-      load_a(0, 0);
-#pragma unroll
-      for (int i = 0; i < WM; ++i) {
-        if (i + 1 < WM) load_a(i + 1, (i + 1) & 1);
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = mfma_fp4<0>(af[i & 1][0], bf[j][0], acc[i][j], sav[i & 1], sbv[j]);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = mfma_fp4<1>(af[i & 1][1], bf[j][1], acc[i][j], sav[i & 1], sbv[j]);
-      }
-    };
-
-#pragma unroll
-    for (int s = 0; s < S - 1; ++s) issue(s, s);
-    for (int k0 = 0; k0 < nk; k0 += S) {
-#pragma unroll
-      for (int s = 0; s < S; ++s) {
-        if (k0 + s < nk) {
-          wait_loads_barrier<(S - 2) * kLoads>();
-          issue((s + S - 1) % S, k0 + s + S - 1);
-          compute(s);
+      for (int u = 0; u < U; ++u) {
+        if (k0 + u < nk) {
+          if (S > 2 && k0 + u + 1 < nk) wait_loads_barrier<(S - 2) * kLoads>();
+          else wait_loads_barrier<0>();
+          feed((u + S - 1) % S, k0 + u + S - 1);
+          compute(u % S, u / 2 % 2, u % 2);
         }
       }
     }
-    wait_loads_barrier<0>();                   // nothing in flight, and every wave done, before the next tile's loads
+    wait_loads_barrier<0>();                   // every wave is done with the stages
+    const Tile d = t;
+    if (i0 + G < total) {                      // the next tile's first loads, before this tile's results go out
+      t = tile_at<BM>(a, start, i0 + G);
+      aim(t);
+#pragma unroll
+      for (int s = 0; s < S - 1; ++s) feed(s, s);
+    }
 
-    // lane (g, c) of sub-tile (i, j) holds rows 4g .. 4g+3 of i and column c of j
+    // lane (g, c) of sub-tile (i, j): row c of i, columns 4g .. 4g+3 of j
+    const bool vec = a.R % 4 == 0;
 #pragma unroll
-    for (int i = 0; i < WM; ++i)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int row = m0 + (BM / 2) * wm + 16 * i + 4 * lg + r;
-        if (row >= n_rows) continue;
-        uint16_t* yr = a.y + (size_t)(first + row) * a.R;
-        if (a.silu) {
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int c = tile_n * (BN / 2) + 32 * wn + 16 * j + rl;
-            if (c < a.R) yr[c] = pq::bf16_rne(pq::silu_mul_f32(acc[i][j][r], acc[i][j + 2][r]));
-          }
+    for (int i = 0; i < WM; ++i) {
+      const int row = d.m0 + (BM / 2) * wm + 16 * i + rl;
+      if (row >= d.n_rows) continue;
+      uint16_t* yr = a.y + (size_t)(d.first + row) * a.R;
+      auto put = [&](int n, floatx4 v) {
+        if (vec) {
+          if (n < a.R) *reinterpret_cast<uint2*>(yr + n) = make_uint2(pq::bf16_pack(v[0], v[1]), pq::bf16_pack(v[2], v[3]));
         } else {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int n = tile_n * BN + 64 * wn + 16 * j + rl;
-            if (n < a.N) yr[n] = pq::bf16_rne(acc[i][j][r]);
-          }
+          for (int r = 0; r < 4; ++r)
+            if (n + r < a.R) yr[n + r] = pq::bf16_rne(v[r]);
         }
+      };
+      if (a.silu) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          floatx4 h;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) h[r] = pq::silu_mul_f32(acc[i][j][r], acc[i][j + 2][r]);
+          put(d.tile_n * (BN / 2) + 32 * wn + 16 * j + 4 * lg, h);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) put(d.tile_n * BN + 64 * wn + 16 * j + 4 * lg, acc[i][j]);
       }
+    }
   }
   zero_tail(a, kThreads);
 }
@@ -431,13 +479,14 @@ long most_row_tiles(const GArgs& a, int tile) {
 template <int BM, int S>
 int launch_tiled(GArgs& a, int num_cus, hipStream_t stream) {
   constexpr size_t kLds = sizeof(Stages<BM, S>);
-  static_assert(kLds + (kMaxExperts + 1) * 4 + 256 <= 160 * 1024, "stages must fit LDS");
+  static_assert(kLds + (kMaxExperts + 1) * 4 + 256 <= 160 * 1024, "stages and tile table must fit LDS");
   auto kern = gemm_mxfp4_tiled_kernel<BM, S>;
   static pqhost::KernelAttrOnce attr;
-  PQ_HIP_CHECK(pqhost::set_dynamic_lds_once(attr, (const void*)kern, (int)kLds));
+  PQ_HIP_CHECK(pqhost::set_dynamic_lds_once(attr, (const void*)kern, (int)(kLds + (kMaxExperts + 1) * 4)));
   a.tn = a.silu ? (a.R + BN / 2 - 1) / (BN / 2) : (a.N + BN - 1) / BN;
   const long most = most_row_tiles(a, BM) * a.tn;
-  hipLaunchKernelGGL(kern, dim3((unsigned)(most < num_cus ? most : num_cus)), dim3(kThreads), kLds, stream, a);
+  hipLaunchKernelGGL(kern, dim3((unsigned)(most < num_cus ? most : num_cus)), dim3(kThreads), kLds + (a.E + 1) * 4,
+                     stream, a);
   PQ_HIP_CHECK(hipGetLastError());
   return PQ_OK;
 }
@@ -452,9 +501,8 @@ int run(GArgs& a, int epi, hipStream_t stream) {
     const char* f = getenv("PQ_MX_BM");
     int bm = f ? atoi(f) : 256;
     if (bm == 256) return launch_tiled<256, 2>(a, dev.num_cus, stream);
-    if (bm == 128) return launch_tiled<128, 3>(a, dev.num_cus, stream);
-    if (bm == 64) return launch_tiled<64, 3>(a, dev.num_cus, stream);
-    return launch_tiled<32, 4>(a, dev.num_cus, stream);
+    if (bm == 128) return launch_tiled<128, 2>(a, dev.num_cus, stream);
+    return launch_tiled<64, 3>(a, dev.num_cus, stream);
   }
   a.tn = a.silu ? (a.R + kPlainTile / 2 - 1) / (kPlainTile / 2) : (a.N + kPlainTile - 1) / kPlainTile;
   const long most = most_row_tiles(a, kPlainTile) * a.tn;

@@ -48,6 +48,15 @@ __device__ __forceinline__ uint4 mx_bf16x8(uint32_t w, float scale) {
   return r;
 }
 
-__device__ __forceinline__ float silu_mul_f32(float g, float u) { return g / (1.0f + __expf(-g)) * u; }
+// silu(g) * u with the hardware reciprocal (1 ulp)
+__device__ __forceinline__ float silu_mul_f32(float g, float u) {
+  return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
+}
+
+// two fp32 values rounded to bf16 (nearest, ties to even), a in the low half
+__device__ __forceinline__ uint32_t bf16_pack(float a, float b) {
+  const bf16x2 p = {(__bf16)a, (__bf16)b};
+  return __builtin_bit_cast(uint32_t, p);
+}
 
 }  // namespace pq
