@@ -35,11 +35,13 @@ namespace {
 
 typedef int int32x8 __attribute__((ext_vector_type(8)));
 typedef float floatx4 __attribute__((ext_vector_type(4)));
+typedef unsigned int int32x4u __attribute__((ext_vector_type(4)));
 
 constexpr int kMaxExperts = 1024;
 constexpr int kThreads = 512;          // tiled kernel
 constexpr int BN = 256;
 constexpr int kRowBytes = 128;         // one K step of a row
+constexpr int kMaxTiledR = 1 << 22;    // 128 result rows are addressed with 32 bits
 constexpr int kXcds = 8;
 constexpr int kGroupM = 8;             // row tiles gone through before the next column tile
 // plain kernel: 4 waves, 2 x 2, 32 x 32 each
@@ -199,7 +201,7 @@ __device__ __forceinline__ Tile tile_at(const GArgs& a, const int* start, int i)
   return t;
 }
 
-template <int BM, int S>
+template <int BM, int S, bool SILU>
 __global__ __launch_bounds__(kThreads) void gemm_mxfp4_tiled_kernel(GArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   Stages<BM, S>& st = *reinterpret_cast<Stages<BM, S>*>(smem);
@@ -355,34 +357,55 @@ __global__ __launch_bounds__(kThreads) void gemm_mxfp4_tiled_kernel(GArgs a) {
       for (int s = 0; s < S - 1; ++s) feed(s, s);
     }
 
-    // lane (g, c) of sub-tile (i, j): row c of i, columns 4g .. 4g+3 of j
-    const bool vec = a.R % 4 == 0;
+    // Results.  Lane (g, c) of sub-tile (i, j) holds row c of i, columns 4g ..
+    // 4g+3 of j: 32 bytes of a row per store instruction.  So 4 KB at a time go
+    // through the wave's part of the last stage (not loaded again before the
+    // next barrier) and out as lines; its 16-byte slots are swizzled by row
+    // like the operands'.
+    constexpr int CW = SILU ? 2 : 4;                         // 16-column sub-tiles of results
+    constexpr int ROWB = 32 * CW, SLOTS = 2 * CW;            // bytes and slots of a row of the box
+    constexpr int RI = SILU ? (WM < 4 ? WM : 4) : 2;         // row sub-tiles in the box
+    constexpr int PER = pq::kWave / SLOTS;                   // rows of a store instruction
+    const int left = max(d.n_rows - d.m0 - (BM / 2) * wm, 0);   // rows of the wave's part that exist
+    // a buffer of those rows: a store behind them is dropped
+    const pq::rsrc_t yr = pq::make_rsrc(a.y + (size_t)(d.first + d.m0 + (BM / 2) * wm) * a.R,
+                                        (uint32_t)min(left, BM / 2) * (uint32_t)a.R * 2u);
+    uint8_t* box = st.b[S - 1] + wv * 4096;
+    const int col = d.tile_n * (SILU ? BN / 2 : BN) + 16 * CW * wn + 8 * (lane % SLOTS);
+    const uint32_t to = col < a.R ? (uint32_t)(lane / SLOTS) * (uint32_t)a.R * 2u + 2u * (uint32_t)col : pq::kOOB;
+    auto swz = [](int r) { return SILU ? (r >> 1) & 3 : r & 7; };
 #pragma unroll
-    for (int i = 0; i < WM; ++i) {
-      const int row = d.m0 + (BM / 2) * wm + 16 * i + rl;
-      if (row >= d.n_rows) continue;
-      uint16_t* yr = a.y + (size_t)(d.first + row) * a.R;
-      auto put = [&](int n, floatx4 v) {
-        if (vec) {
-          if (n < a.R) *reinterpret_cast<uint2*>(yr + n) = make_uint2(pq::bf16_pack(v[0], v[1]), pq::bf16_pack(v[2], v[3]));
+    for (int i0 = 0; i0 < WM; i0 += RI) {
+#pragma unroll
+      for (int i = i0; i < i0 + RI; ++i)
+#pragma unroll
+        for (int j = 0; j < CW; ++j) {
+          floatx4 h = acc[i][j];
+          if (SILU) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) h[r] = pq::silu_mul_f32(acc[i][j][r], acc[i][j + 4 - CW][r]);
+          }
+          const int r = 16 * (i - i0) + rl, sl = (2 * j + (lg >> 1)) ^ swz(r);
+          *reinterpret_cast<uint2*>(box + ROWB * r + 16 * sl + 8 * (lg & 1)) =
+              make_uint2(pq::bf16_pack(h[0], h[1]), pq::bf16_pack(h[2], h[3]));
+        }
+      asm volatile("" ::: "memory");
+#pragma unroll
+      for (int q = 0; q < 16 * RI / PER; ++q) {
+        const int r = PER * q + lane / SLOTS;
+        const uint4 v = *reinterpret_cast<const uint4*>(box + ROWB * r + 16 * ((lane % SLOTS) ^ swz(r)));
+        const int down = (16 * i0 + PER * q) * a.R * 2;
+        if (a.R % 8 == 0) {
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(int32x4u, v), yr, (int)to, down, 0);
         } else {
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-          for (int r = 0; r < 4; ++r)
-            if (n + r < a.R) yr[n + r] = pq::bf16_rne(v[r]);
+          for (int c = 0; c < 8; ++c)
+            if (col + c < a.R)
+              __builtin_amdgcn_raw_buffer_store_b16((short)(uint16_t)(w[c >> 1] >> (16 * (c & 1))), yr, (int)(to + 2 * c), down, 0);
         }
-      };
-      if (a.silu) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          floatx4 h;
-#pragma unroll
-          for (int r = 0; r < 4; ++r) h[r] = pq::silu_mul_f32(acc[i][j][r], acc[i][j + 2][r]);
-          put(d.tile_n * (BN / 2) + 32 * wn + 16 * j + 4 * lg, h);
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) put(d.tile_n * BN + 64 * wn + 16 * j + 4 * lg, acc[i][j]);
       }
+      asm volatile("" ::: "memory");
     }
   }
   zero_tail(a, kThreads);
@@ -476,11 +499,11 @@ long most_row_tiles(const GArgs& a, int tile) {
   return (long)a.P / tile + (a.E < a.P ? a.E : a.P);
 }
 
-template <int BM, int S>
-int launch_tiled(GArgs& a, int num_cus, hipStream_t stream) {
+template <int BM, int S, bool SILU>
+int launch_tiled_as(GArgs& a, int num_cus, hipStream_t stream) {
   constexpr size_t kLds = sizeof(Stages<BM, S>);
   static_assert(kLds + (kMaxExperts + 1) * 4 + 256 <= 160 * 1024, "stages and tile table must fit LDS");
-  auto kern = gemm_mxfp4_tiled_kernel<BM, S>;
+  auto kern = gemm_mxfp4_tiled_kernel<BM, S, SILU>;
   static pqhost::KernelAttrOnce attr;
   PQ_HIP_CHECK(pqhost::set_dynamic_lds_once(attr, (const void*)kern, (int)(kLds + (kMaxExperts + 1) * 4)));
   a.tn = a.silu ? (a.R + BN / 2 - 1) / (BN / 2) : (a.N + BN - 1) / BN;
@@ -491,13 +514,18 @@ int launch_tiled(GArgs& a, int num_cus, hipStream_t stream) {
   return PQ_OK;
 }
 
+template <int BM, int S>
+int launch_tiled(GArgs& a, int num_cus, hipStream_t stream) {
+  return a.silu ? launch_tiled_as<BM, S, true>(a, num_cus, stream) : launch_tiled_as<BM, S, false>(a, num_cus, stream);
+}
+
 int run(GArgs& a, int epi, hipStream_t stream) {
   pqhost::DeviceInfo dev;
   const int st = pqhost::current_device_info(&dev);
   if (st != PQ_OK) return st;
   a.silu = epi == PQ_EPI_SILU_MUL;
   a.R = a.silu ? a.N / 2 : a.N;
-  if (a.K % 128 == 0) {
+  if (a.K % 128 == 0 && a.R <= kMaxTiledR) {
     const char* f = getenv("PQ_MX_BM");
     int bm = f ? atoi(f) : 256;
     if (bm == 256) return launch_tiled<256, 2>(a, dev.num_cus, stream);
