@@ -425,7 +425,9 @@ size_t pq_gemm_mxfp4_workspace(int M, int K, int N, int epi);
  *       the workspace of the other entry points; calls that share it must be
  *       ordered (one stream).
  * Constraints: K % 32 == 0, N >= 1, N*K/2 < 2^31, M*K/2 < 2^31, N even under
- * PQ_EPI_SILU_MUL.  An output's bits do not depend on the other tokens. */
+ * PQ_EPI_SILU_MUL.  An output's bits do not depend on the other tokens.  A
+ * tiled kernel where K % 128 == 0 (PQ_MXFP4_TILE=1..4 forces one of its tiles:
+ * 64 x 128, 64 x 256, 128 x 256, 256 x 256; equal bits), a plain one elsewhere. */
 int pq_gemm_mxfp4(const uint16_t* x, int M, int K,
                   const uint8_t* w, const uint8_t* w_scale, int N,
                   int epi, uint16_t* y, void* ws, size_t ws_bytes, void* stream);

@@ -10,8 +10,9 @@
 // Two kernels.  The tiled one (K % 128 == 0, so that scale rows are whole
 // dwords):
 //   * a 512-thread block (8 waves, 2 along the rows x 4 along the columns) owns
-//     a BM x 256 tile, BM = 256, 128, 64 or 32; a K step is 256 values, 128
-//     bytes of each row: whole lines;
+//     a tile of 64 x 128 up to 256 x 256; a K step is 256 values, 128 bytes of
+//     each row: whole lines (half lines, 128 values a step with more stages,
+//     took 824 us where these take 766);
 //   * codes and scales stream from memory straight into LDS (buffer loads with
 //     an LDS destination), S stages deep, one block barrier per step; the wait
 //     leaves the younger stages in flight.  The 16-byte piece c of row r lands
@@ -39,7 +40,6 @@ typedef unsigned int int32x4u __attribute__((ext_vector_type(4)));
 
 constexpr int kMaxExperts = 1024;
 constexpr int kThreads = 512;          // tiled kernel
-constexpr int BN = 256;
 constexpr int kRowBytes = 128;         // one K step of a row
 constexpr int kMaxTiledR = 1 << 22;    // 128 result rows are addressed with 32 bits
 constexpr int kXcds = 8;
@@ -162,10 +162,11 @@ __device__ __forceinline__ void zero_tail(const GArgs& a, int threads) {
 // every stage are one register plus a constant.  A scale buffer holds two
 // steps (16 bytes of a row): a row's scale line is then read from L2 half as
 // often as with one step a time (the L1 does not hold it that long).
-template <int BM, int S>
+template <int BM, int BN, int S>
 struct Stages {
   uint8_t a[S][BM * kRowBytes];
   uint8_t b[S][BN * kRowBytes];
+  static_assert(S <= 3, "two scale buffers hold the steps in flight");
   uint8_t sa[2][BM * 16];
   uint8_t sb[2][BN * 16];
 };
@@ -201,14 +202,16 @@ __device__ __forceinline__ Tile tile_at(const GArgs& a, const int* start, int i)
   return t;
 }
 
-template <int BM, int S, bool SILU>
+template <int BM, int BN, int S, bool SILU>
 __global__ __launch_bounds__(kThreads) void gemm_mxfp4_tiled_kernel(GArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
-  Stages<BM, S>& st = *reinterpret_cast<Stages<BM, S>*>(smem);
-  int* start = reinterpret_cast<int*>(smem + sizeof(Stages<BM, S>));   // [E + 1]
+  Stages<BM, BN, S>& st = *reinterpret_cast<Stages<BM, BN, S>*>(smem);
+  int* start = reinterpret_cast<int*>(smem + sizeof(Stages<BM, BN, S>));   // [E + 1]
   constexpr int WM = BM / 32;                  // 16-row sub-tiles per wave
   constexpr int LA = BM / 64;                  // A loads of a wave and stage
-  constexpr int kLoads = LA + BN / 64;         // code loads of a wave and stage
+  constexpr int LB = BN / 64;
+  constexpr int kLoads = LA + LB;              // code loads of a wave and stage
+  constexpr int CN = BN / 64;                  // 16-column sub-tiles per wave; under SiLU*up gates, then ups
   tile_starts<BM, kThreads>(a, start);
   const int lane = pq::lane_id();
   const int wv = __builtin_amdgcn_readfirstlane(pq::wave_id());
@@ -230,12 +233,12 @@ __global__ __launch_bounds__(kThreads) void gemm_mxfp4_tiled_kernel(GArgs a) {
 
   // operand reads of this lane: pieces 2g and 2g + 1 of its rows, and their scale bytes
   const uint32_t sw0 = 16u * (uint32_t)((2 * lg) ^ (rl & 7)), sw1 = 16u * (uint32_t)((2 * lg + 1) ^ (rl & 7));
-  const int ar = (BM / 2) * wm + rl, br = 64 * wn + rl;
+  const int ar = (BM / 2) * wm + rl, br = 16 * CN * wn + rl;
   const uint8_t *pa0 = st.a[0] + ar * kRowBytes + sw0, *pa1 = st.a[0] + ar * kRowBytes + sw1;
   const uint8_t *pb0 = st.b[0] + br * kRowBytes + sw0, *pb1 = st.b[0] + br * kRowBytes + sw1;
   const uint8_t *psa = st.sa[0] + ar * 16 + 2 * lg, *psb = st.sb[0] + br * 16 + 2 * lg;
 
-  uint32_t aoff[LA], boff[BN / 64], soff;
+  uint32_t aoff[LA], boff[LB], soff;
   pq::int32x4 wr, wsr;
   auto aim = [&](const Tile& t) {
     wr = pq::rsrc_words(a.w + (size_t)t.e * a.N * rowb, (uint32_t)((size_t)a.N * rowb));
@@ -246,11 +249,11 @@ __global__ __launch_bounds__(kThreads) void gemm_mxfp4_tiled_kernel(GArgs a) {
       aoff[i] = r >= 0 ? (uint32_t)r * rowb + 16u * piece : pq::kOOB;
     }
 #pragma unroll
-    for (int i = 0; i < BN / 64; ++i) {
-      const int r = b_row<BN, 32>(a, t.tile_n, 64 * i + row_l);
+    for (int i = 0; i < LB; ++i) {
+      const int r = b_row<BN, BN / 8>(a, t.tile_n, 64 * i + row_l);
       boff[i] = r >= 0 ? (uint32_t)r * rowb + 16u * piece : pq::kOOB;
     }
-    const int r = wv >= LA + BN / 64 ? -1 : s_a ? x_row(a, t.first, t.n_rows, t.m0 + srow) : b_row<BN, 32>(a, t.tile_n, srow);
+    const int r = wv >= LA + LB ? -1 : s_a ? x_row(a, t.first, t.n_rows, t.m0 + srow) : b_row<BN, BN / 8>(a, t.tile_n, srow);
     soff = r >= 0 ? (uint32_t)r * nb : pq::kOOB;
   };
 
@@ -263,14 +266,14 @@ __global__ __launch_bounds__(kThreads) void gemm_mxfp4_tiled_kernel(GArgs a) {
     for (int i = 0; i < LA; ++i)
       pq::dma16(xr, pq::lds_addr(st.a[s] + (64 * i + 8 * wv) * kRowBytes), ok ? aoff[i] : pq::kOOB, kofs);
 #pragma unroll
-    for (int i = 0; i < BN / 64; ++i)
+    for (int i = 0; i < LB; ++i)
       pq::dma16(wr, pq::lds_addr(st.b[s] + (64 * i + 8 * wv) * kRowBytes), ok ? boff[i] : pq::kOOB, kofs);
   };
   // the scales of steps 2p and 2p + 1 into buffer p % 2: 16 bytes a row, the
   // last ones as dwords, with zeros past K (a zero code times another row's NaN
   // scale would be NaN)
   auto issue_scales = [&](int p) {
-    if (16 * p >= nb || wv >= LA + BN / 64) return;
+    if (16 * p >= nb || wv >= LA + LB) return;
     uint8_t* to = s_a ? st.sa[p & 1] + wv * 1024 : st.sb[p & 1] + (wv - LA) * 1024;
     const pq::int32x4 r = {s_a ? xsr[0] : wsr[0], s_a ? xsr[1] : wsr[1], s_a ? xsr[2] : wsr[2], 0x00020000};
     const uint32_t pofs = (uint32_t)__builtin_amdgcn_readfirstlane(16 * p);
@@ -291,22 +294,22 @@ __global__ __launch_bounds__(kThreads) void gemm_mxfp4_tiled_kernel(GArgs a) {
     issue(s, k);
   };
 
-  floatx4 acc[WM][4];
+  floatx4 acc[WM][CN];
   // the A reads of sub-tile i + 1 are issued before the products of sub-tile i.
   // The weights are the first operand: a lane then holds four consecutive
   // outputs of one row
   auto compute = [&](int s, int buf, int odd) {
     const int ab = s * BM * kRowBytes, bb = s * BN * kRowBytes;
     const uint8_t *qa = psa + buf * BM * 16 + 8 * odd, *qb = psb + buf * BN * 16 + 8 * odd;
-    uint4 af[2][2], bf[4][2];
-    uint32_t sav[2], sbv[4];
+    uint4 af[2][2], bf[CN][2];
+    uint32_t sav[2], sbv[CN];
     auto load_a = [&](int i, int q) {
       af[q][0] = *reinterpret_cast<const uint4*>(pa0 + ab + 16 * i * kRowBytes);
       af[q][1] = *reinterpret_cast<const uint4*>(pa1 + ab + 16 * i * kRowBytes);
       sav[q] = *reinterpret_cast<const uint16_t*>(qa + 16 * i * 16);
     };
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < CN; ++j) {
       bf[j][0] = *reinterpret_cast<const uint4*>(pb0 + bb + 16 * j * kRowBytes);
       bf[j][1] = *reinterpret_cast<const uint4*>(pb1 + bb + 16 * j * kRowBytes);
       sbv[j] = *reinterpret_cast<const uint16_t*>(qb + 16 * j * 16);
@@ -317,9 +320,9 @@ __global__ __launch_bounds__(kThreads) void gemm_mxfp4_tiled_kernel(GArgs a) {
       if (i + 1 < WM) load_a(i + 1, (i + 1) & 1);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] = mfma_fp4<0>(bf[j][0], af[i & 1][0], acc[i][j], sbv[j], sav[i & 1]);
+      for (int j = 0; j < CN; ++j) acc[i][j] = mfma_fp4<0>(bf[j][0], af[i & 1][0], acc[i][j], sbv[j], sav[i & 1]);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] = mfma_fp4<1>(bf[j][1], af[i & 1][1], acc[i][j], sbv[j], sav[i & 1]);
+      for (int j = 0; j < CN; ++j) acc[i][j] = mfma_fp4<1>(bf[j][1], af[i & 1][1], acc[i][j], sbv[j], sav[i & 1]);
     }
   };
 
@@ -334,14 +337,14 @@ __global__ __launch_bounds__(kThreads) void gemm_mxfp4_tiled_kernel(GArgs a) {
 #pragma unroll
     for (int i = 0; i < WM; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
-    // unrolled over the stages and the two steps of a scale buffer
+      for (int j = 0; j < CN; ++j) acc[i][j] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+    // unrolled over the stages and the two steps of each scale buffer, which go by a step's place
     constexpr int U = S % 2 == 0 ? 2 * S : 4 * S;
     for (int k0 = 0; k0 < nk; k0 += U) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         if (k0 + u < nk) {
-          if (S > 2 && k0 + u + 1 < nk) wait_loads_barrier<(S - 2) * kLoads>();
+          if (S > 2 && k0 + u + S - 2 < nk) wait_loads_barrier<(S - 2) * kLoads>();
           else wait_loads_barrier<0>();
           feed((u + S - 1) % S, k0 + u + S - 1);
           compute(u % S, u / 2 % 2, u % 2);
@@ -358,22 +361,22 @@ __global__ __launch_bounds__(kThreads) void gemm_mxfp4_tiled_kernel(GArgs a) {
     }
 
     // Results.  Lane (g, c) of sub-tile (i, j) holds row c of i, columns 4g ..
-    // 4g+3 of j: 32 bytes of a row per store instruction.  So 4 KB at a time go
+    // 4g+3 of j: 32 bytes of a row per store instruction.  So up to 4 KB at a time go
     // through the wave's part of the last stage (not loaded again before the
     // next barrier) and out as lines; its 16-byte slots are swizzled by row
     // like the operands'.
-    constexpr int CW = SILU ? 2 : 4;                         // 16-column sub-tiles of results
+    constexpr int CW = SILU ? CN / 2 : CN;                   // 16-column sub-tiles of results
     constexpr int ROWB = 32 * CW, SLOTS = 2 * CW;            // bytes and slots of a row of the box
-    constexpr int RI = SILU ? (WM < 4 ? WM : 4) : 2;         // row sub-tiles in the box
+    constexpr int RI = WM < BN / ROWB ? WM : BN / ROWB;      // row sub-tiles in the box
     constexpr int PER = pq::kWave / SLOTS;                   // rows of a store instruction
     const int left = max(d.n_rows - d.m0 - (BM / 2) * wm, 0);   // rows of the wave's part that exist
     // a buffer of those rows: a store behind them is dropped
     const pq::rsrc_t yr = pq::make_rsrc(a.y + (size_t)(d.first + d.m0 + (BM / 2) * wm) * a.R,
                                         (uint32_t)min(left, BM / 2) * (uint32_t)a.R * 2u);
-    uint8_t* box = st.b[S - 1] + wv * 4096;
+    uint8_t* box = st.b[S - 1] + wv * (BN * kRowBytes / (kThreads / pq::kWave));
     const int col = d.tile_n * (SILU ? BN / 2 : BN) + 16 * CW * wn + 8 * (lane % SLOTS);
     const uint32_t to = col < a.R ? (uint32_t)(lane / SLOTS) * (uint32_t)a.R * 2u + 2u * (uint32_t)col : pq::kOOB;
-    auto swz = [](int r) { return SILU ? (r >> 1) & 3 : r & 7; };
+    auto swz = [](int r) { return r / (8 / SLOTS) % SLOTS; };
 #pragma unroll
     for (int i0 = 0; i0 < WM; i0 += RI) {
 #pragma unroll
@@ -383,7 +386,7 @@ __global__ __launch_bounds__(kThreads) void gemm_mxfp4_tiled_kernel(GArgs a) {
           floatx4 h = acc[i][j];
           if (SILU) {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) h[r] = pq::silu_mul_f32(acc[i][j][r], acc[i][j + 4 - CW][r]);
+            for (int r = 0; r < 4; ++r) h[r] = pq::silu_mul_f32(acc[i][j][r], acc[i][j + CN - CW][r]);
           }
           const int r = 16 * (i - i0) + rl, sl = (2 * j + (lg >> 1)) ^ swz(r);
           *reinterpret_cast<uint2*>(box + ROWB * r + 16 * sl + 8 * (lg & 1)) =
@@ -499,11 +502,11 @@ long most_row_tiles(const GArgs& a, int tile) {
   return (long)a.P / tile + (a.E < a.P ? a.E : a.P);
 }
 
-template <int BM, int S, bool SILU>
+template <int BM, int BN, int S, bool SILU>
 int launch_tiled_as(GArgs& a, int num_cus, hipStream_t stream) {
-  constexpr size_t kLds = sizeof(Stages<BM, S>);
+  constexpr size_t kLds = sizeof(Stages<BM, BN, S>);
   static_assert(kLds + (kMaxExperts + 1) * 4 + 256 <= 160 * 1024, "stages and tile table must fit LDS");
-  auto kern = gemm_mxfp4_tiled_kernel<BM, S, SILU>;
+  auto kern = gemm_mxfp4_tiled_kernel<BM, BN, S, SILU>;
   static pqhost::KernelAttrOnce attr;
   PQ_HIP_CHECK(pqhost::set_dynamic_lds_once(attr, (const void*)kern, (int)(kLds + (kMaxExperts + 1) * 4)));
   a.tn = a.silu ? (a.R + BN / 2 - 1) / (BN / 2) : (a.N + BN - 1) / BN;
@@ -514,9 +517,9 @@ int launch_tiled_as(GArgs& a, int num_cus, hipStream_t stream) {
   return PQ_OK;
 }
 
-template <int BM, int S>
+template <int BM, int BN, int S>
 int launch_tiled(GArgs& a, int num_cus, hipStream_t stream) {
-  return a.silu ? launch_tiled_as<BM, S, true>(a, num_cus, stream) : launch_tiled_as<BM, S, false>(a, num_cus, stream);
+  return a.silu ? launch_tiled_as<BM, BN, S, true>(a, num_cus, stream) : launch_tiled_as<BM, BN, S, false>(a, num_cus, stream);
 }
 
 int run(GArgs& a, int epi, hipStream_t stream) {
@@ -526,11 +529,31 @@ int run(GArgs& a, int epi, hipStream_t stream) {
   a.silu = epi == PQ_EPI_SILU_MUL;
   a.R = a.silu ? a.N / 2 : a.N;
   if (a.K % 128 == 0 && a.R <= kMaxTiledR) {
-    const char* f = getenv("PQ_MX_BM");
-    int bm = f ? atoi(f) : 256;
-    if (bm == 256) return launch_tiled<256, 2>(a, dev.num_cus, stream);
-    if (bm == 128) return launch_tiled<128, 2>(a, dev.num_cus, stream);
-    return launch_tiled<64, 3>(a, dev.num_cus, stream);
+    // Tile by the rows an expert has on average and by the tiles there are:
+    // small tiles while they all run at once (333 tokens 5120 -> 5120: 64 x 128
+    // tiles 15.4 us, 64 x 256 21.3, 128 x 256 25.8; 1024 tokens: 128 x 256 28.7,
+    // 64 x 256 40.7, 256 x 256 38.6); past that the height that an expert's rows
+    // fill, since every row tile streams the expert's weights again (experts of
+    // 62 rows: 64 x 256 67.6 us, 128 x 256 83.8; of 187: 133.9, 108.2, 256 x 256
+    // 113.3; of 512: 338, 270, 229).
+    const long used = a.E < a.P ? a.E : a.P, avg = (a.P + used - 1) / used;
+    auto tiles = [&](long bm, long bn) {
+      const long cols = a.silu ? bn / 2 : bn;
+      return used * ((avg + bm - 1) / bm) * ((a.R + cols - 1) / cols);
+    };
+    const char* force = getenv("PQ_MXFP4_TILE");
+    int pick = force ? atoi(force) : 0;
+    if (pick == 0)
+      pick = tiles(64, 128) <= dev.num_cus                 ? 1
+             : avg <= 64 || tiles(64, 256) <= dev.num_cus   ? 2
+             : avg <= 256 || tiles(128, 256) <= dev.num_cus ? 3
+                                                            : 4;
+    switch (pick) {
+      case 1: return launch_tiled<64, 128, 3>(a, dev.num_cus, stream);
+      case 2: return launch_tiled<64, 256, 3>(a, dev.num_cus, stream);
+      case 3: return launch_tiled<128, 256, 2>(a, dev.num_cus, stream);
+      default: return launch_tiled<256, 256, 2>(a, dev.num_cus, stream);
+    }
   }
   a.tn = a.silu ? (a.R + kPlainTile / 2 - 1) / (kPlainTile / 2) : (a.N + kPlainTile - 1) / kPlainTile;
   const long most = most_row_tiles(a, kPlainTile) * a.tn;

@@ -213,6 +213,33 @@ def test_gemm(pq, M, K, N, silu):
         assert torch.equal(pq.gemm_mxfp4(x[cut:].contiguous(), w, s, epi), y[cut:])
 
 
+@pytest.mark.parametrize("silu", [False, True])
+@pytest.mark.parametrize("M,K,N", [(65, 128, 260), (130, 640, 520), (300, 896, 390), (513, 1152, 774)])
+def test_gemm_tiles_agree(pq, monkeypatch, M, K, N, silu):
+    """Every tile of the tiled kernel gives the same bits, and leaves what lies around the output alone."""
+    import torch
+    rng = np.random.default_rng(M)
+    x, _ = _bf16(rng.standard_normal((M, K)))
+    w, s, _ = _weights(rng, N, K)
+    epi = pq.EPI_SILU_MUL if silu else pq.EPI_NONE
+    xq, xs = pq.quantize_mxfp4(x)
+    R = N // 2 if silu else N
+    want, bound = expect(oracle.mx_values(xq.cpu().numpy(), xs.cpu().numpy()),
+                         oracle.mx_values(w.cpu().numpy(), s.cpu().numpy()), silu)
+    seen = []
+    for tile in ("1", "2", "3", "4"):
+        monkeypatch.setenv("PQ_MXFP4_TILE", tile)
+        room = torch.full((M + 600, R), 7.0, dtype=torch.bfloat16, device="cuda")
+        pad = 304                                           # a multiple of 8: the output stays 16-byte aligned
+        out = room[pad:pad + M]
+        assert out.data_ptr() % 16 == 0
+        y = pq.gemm_mxfp4_prequant(xq, xs, w, s, epi, out=out)
+        assert (room[:pad] == 7.0).all() and (room[pad + M:] == 7.0).all()
+        close(y, want, bound, f"tile {tile}")
+        seen.append(y.clone())
+    assert all(torch.equal(y, seen[0]) for y in seen)
+
+
 def test_gemm_nan_rows_stay_alone(pq):
     import torch
     rng = np.random.default_rng(8)
