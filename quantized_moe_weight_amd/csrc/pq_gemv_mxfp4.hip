@@ -9,7 +9,7 @@
 //     bf16 pair (exact), so a weight costs half a vector instruction whatever
 //     M is, and the block scales ride along;
 //   * a block owns a contiguous range of output rows, cut into tiles of at
-//     most 16 rows of equal size; the (tile, 256-value step) units are dealt to
+//     most 16 rows of equal size; the (tile, K step) units are dealt to
 //     its waves as contiguous runs, and tiles cut between waves are added
 //     through LDS in wave order after one barrier: no global partials;
 //   * a wave's load covers 8 rows x 128 bytes (whole lines): lane (g, r)
@@ -31,7 +31,7 @@ constexpr int kWaves = kThreads / pq::kWave;
 constexpr int kMaxM = 16;
 constexpr long kMaxMK = 69632;         // M*K bound: the activation lives in one CU's LDS
 constexpr int kTile = 16;              // weight rows per tile
-constexpr int kStep = 256;             // values of K per step (128 bytes of each row)
+constexpr int kHalf = 256;             // values of K in 128 bytes of a row
 
 struct MxArgs {
   const uint16_t* x;
@@ -53,8 +53,12 @@ __device__ __forceinline__ floatx4 mfma16(uint4 a, uint4 b, floatx4 c) {
 __device__ __forceinline__ uint32_t ror8(uint32_t v) { return (uint32_t)pq::dpp_i32<0x128>((int)v); }
 
 // NROW: 2 under SiLU*up (gate row and up row of the same outputs), else 1.
-// D: steps in flight per wave.
-template <int NROW, int D>
+// H: 128-byte parts of a row per step; 2 where rows are whole steps (K % 512 ==
+// 0): a row's 16 scale bytes of the step are then one load, where single bytes
+// made the scale lines as much L2 traffic as the codes (4096 -> 151552, M = 1:
+// 63 us against 80.7; 5120 -> 2 x 17408: 21.4 against 26.6).
+// D: steps in flight per wave (deeper rings and 16 waves measured the same).
+template <int NROW, int H, int D>
 __global__ __launch_bounds__(kThreads) void gemv_mxfp4_kernel(MxArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   const int tid = (int)threadIdx.x, lane = pq::lane_id();
@@ -76,26 +80,33 @@ __global__ __launch_bounds__(kThreads) void gemv_mxfp4_kernel(MxArgs a) {
   // ring of weight loads
   const int lrow = r16 & 7, up8 = r16 >> 3;
   int it = nt > 0 ? u0 / a.nk : 0, ik = nt > 0 ? u0 - it * a.nk : 0, ileft = left0;
-  auto issue = [&](uint4 (&wb)[NROW][2], uint32_t (&sb)[NROW][2]) {
+  auto issue = [&](uint4 (&wb)[NROW][H][2], uint32_t (&sb)[NROW][H][2]) {
     const bool ok = ileft > 0;
     const int t0 = ok ? pq::split_start(rows, nt, it) : 0;
     const int tn = ok ? pq::split_start(rows, nt, it + 1) - t0 : 0;
-    const uint32_t p0 = (uint32_t)(8 * ik + g + 4 * up8), p1 = (uint32_t)(8 * ik + g + 4 * (1 - up8));
-    const uint32_t q0 = (uint32_t)(8 * ik + g);
 #pragma unroll
     for (int j = 0; j < NROW; ++j) {
       const uint32_t base = (uint32_t)(rs + t0 + j * a.R);
-      wb[j][0] = pq::buf_load16_nt(wr, lrow < tn && p0 < nsc ? (base + lrow) * rowb + 16u * p0 : pq::kOOB);
-      wb[j][1] = pq::buf_load16_nt(wr, lrow + 8 < tn && p1 < nsc ? (base + 8 + lrow) * rowb + 16u * p1 : pq::kOOB);
-      const uint32_t so = (base + (uint32_t)r16) * nsc + q0;
-      sb[j][0] = __builtin_amdgcn_raw_buffer_load_b8(sr, (int)(r16 < tn && q0 < nsc ? so : pq::kOOB), 0, 0);
-      sb[j][1] = __builtin_amdgcn_raw_buffer_load_b8(sr, (int)(r16 < tn && q0 + 4 < nsc ? so + 4u : pq::kOOB), 0, 0);
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+        const uint32_t q = (uint32_t)(8 * (H * ik + h) + g), p0 = q + 4 * up8, p1 = q + 4 * (1 - up8);
+        wb[j][h][0] = pq::buf_load16_nt(wr, lrow < tn && p0 < nsc ? (base + lrow) * rowb + 16u * p0 : pq::kOOB);
+        wb[j][h][1] = pq::buf_load16_nt(wr, lrow + 8 < tn && p1 < nsc ? (base + 8 + lrow) * rowb + 16u * p1 : pq::kOOB);
+      }
+      if constexpr (H == 2) {
+        const uint4 v = pq::buf_load16(sr, r16 < tn ? (base + (uint32_t)r16) * nsc + 16u * (uint32_t)ik : pq::kOOB);
+        sb[j][0][0] = v.x; sb[j][0][1] = v.y; sb[j][1][0] = v.z; sb[j][1][1] = v.w;
+      } else {
+        const uint32_t q = (uint32_t)(8 * ik + g), so = (base + (uint32_t)r16) * nsc + q;
+        sb[j][0][0] = __builtin_amdgcn_raw_buffer_load_b8(sr, (int)(r16 < tn && q < nsc ? so : pq::kOOB), 0, 0);
+        sb[j][0][1] = __builtin_amdgcn_raw_buffer_load_b8(sr, (int)(r16 < tn && q + 4 < nsc ? so + 4u : pq::kOOB), 0, 0);
+      }
     }
     --ileft;
     if (++ik == a.nk) { ik = 0; ++it; }
   };
-  uint4 wbuf[D][NROW][2];
-  uint32_t sbuf[D][NROW][2];
+  uint4 wbuf[D][NROW][H][2];
+  uint32_t sbuf[D][NROW][H][2];                          // H = 2: the dword of a half's pieces 0-3 and 4-7
 #pragma unroll
   for (int d = 0; d < D; ++d) issue(wbuf[d], sbuf[d]);
   __builtin_amdgcn_sched_barrier(0);
@@ -122,26 +133,30 @@ __global__ __launch_bounds__(kThreads) void gemv_mxfp4_kernel(MxArgs a) {
   for (int j = 0; j < NROW; ++j) acc[j] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
   int ct = nt > 0 ? u0 / a.nk : 0, ck = nt > 0 ? u0 - ct * a.nk : 0, cleft = left0;
 
-  auto consume = [&](const uint4 (&wb)[NROW][2], const uint32_t (&sb)[NROW][2]) {
-    uint4 xa[2][4];
+  auto consume = [&](const uint4 (&wb)[NROW][H][2], const uint32_t (&sb)[NROW][H][2]) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint32_t blk = (uint32_t)(8 * ck + 4 * h + g);
-      const uint8_t* xp = smem + (blk < nsc ? xl + 64u * blk : a.poff - 64u);
+    for (int h = 0; h < H; ++h) {
+      uint4 xa[2][4];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) xa[h][t] = *reinterpret_cast<const uint4*>(xp + 16 * t);
-    }
+      for (int e = 0; e < 2; ++e) {
+        const uint32_t blk = (uint32_t)(8 * (H * ck + h) + 4 * e + g);
+        const uint8_t* xp = smem + (blk < nsc ? xl + 64u * blk : a.poff - 64u);
 #pragma unroll
-    for (int j = 0; j < NROW; ++j) {
-      const uint32_t v0[4] = {wb[j][0].x, wb[j][0].y, wb[j][0].z, wb[j][0].w};
-      const uint32_t v1[4] = {wb[j][1].x, wb[j][1].y, wb[j][1].z, wb[j][1].w};
-      const float s0 = pq::mx_scale_operand(sb[j][0]), s1 = pq::mx_scale_operand(sb[j][1]);
+        for (int t = 0; t < 4; ++t) xa[e][t] = *reinterpret_cast<const uint4*>(xp + 16 * t);
+      }
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const uint32_t lo = up8 ? v1[t] : v0[t];          // piece g of row r16
-        const uint32_t hi = ror8(up8 ? v0[t] : v1[t]);    // piece g + 4, from lane r16 ^ 8
-        acc[j] = mfma16(xa[0][t], pq::mx_bf16x8(lo, s0), acc[j]);
-        acc[j] = mfma16(xa[1][t], pq::mx_bf16x8(hi, s1), acc[j]);
+      for (int j = 0; j < NROW; ++j) {
+        const uint32_t v0[4] = {wb[j][h][0].x, wb[j][h][0].y, wb[j][h][0].z, wb[j][h][0].w};
+        const uint32_t v1[4] = {wb[j][h][1].x, wb[j][h][1].y, wb[j][h][1].z, wb[j][h][1].w};
+        auto scale = [&](uint32_t v) { return pq::mx_scale_operand(H == 2 ? (v >> (8 * g)) & 255u : v); };
+        const float s0 = scale(sb[j][h][0]), s1 = scale(sb[j][h][1]);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const uint32_t lo = up8 ? v1[t] : v0[t];          // piece g of row r16
+          const uint32_t hi = ror8(up8 ? v0[t] : v1[t]);    // piece g + 4, from lane r16 ^ 8
+          acc[j] = mfma16(xa[0][t], pq::mx_bf16x8(lo, s0), acc[j]);
+          acc[j] = mfma16(xa[1][t], pq::mx_bf16x8(hi, s1), acc[j]);
+        }
       }
     }
     --cleft;
@@ -192,9 +207,9 @@ __global__ __launch_bounds__(kThreads) void gemv_mxfp4_kernel(MxArgs a) {
 
 constexpr size_t kMaxLds = 160 * 1024;
 
-template <int NROW, int D>
+template <int NROW, int H, int D>
 hipError_t launch(const MxArgs& a, size_t lds, int grid, hipStream_t stream) {
-  auto kern = gemv_mxfp4_kernel<NROW, D>;
+  auto kern = gemv_mxfp4_kernel<NROW, H, D>;
   static pqhost::KernelAttrOnce attr;
   const hipError_t e = pqhost::set_dynamic_lds_once(attr, (const void*)kern, (int)kMaxLds);
   if (e != hipSuccess) return e;
@@ -223,7 +238,8 @@ int pq_gemv_mxfp4(const uint16_t* x, int M, int K, const uint8_t* w, const uint8
   a.x = x; a.w = w; a.wsc = w_scale; a.y = y;
   a.M = M; a.K = K; a.N = N;
   a.R = silu ? N / 2 : N;
-  a.nk = (K + kStep - 1) / kStep;
+  const bool wide = K % (2 * kHalf) == 0;
+  a.nk = wide ? K / (2 * kHalf) : (K + kHalf - 1) / kHalf;
   a.xstride = (uint32_t)K * 2 + 16;
   a.poff = (uint32_t)M * a.xstride + 64;
   // one block per CU, more where a block's partial sums would not fit its LDS
@@ -238,8 +254,9 @@ int pq_gemv_mxfp4(const uint16_t* x, int M, int K, const uint8_t* w, const uint8
   }
   if (lds > kMaxLds) return PQ_ERR_SHAPE;
   if (grid > a.R) grid = a.R;
-  const hipError_t e = silu ? launch<2, 2>(a, lds, grid, (hipStream_t)stream)
-                            : launch<1, 3>(a, lds, grid, (hipStream_t)stream);
+  hipStream_t sm = (hipStream_t)stream;
+  const hipError_t e = wide ? (silu ? launch<2, 2, 2>(a, lds, grid, sm) : launch<1, 2, 2>(a, lds, grid, sm))
+                            : (silu ? launch<2, 1, 2>(a, lds, grid, sm) : launch<1, 1, 3>(a, lds, grid, sm));
   if (e != hipSuccess) {
     pqhost::set_last_hip_error((int)e);
     return PQ_ERR_HIP;
