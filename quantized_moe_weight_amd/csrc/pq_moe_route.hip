@@ -156,6 +156,19 @@ struct MoveArgs {
   int n16;                 // 16-byte pieces of a row
 };
 
+// 16 bytes that are read, or written, once: the sorted rows pass through the
+// caches (32792 rows of 12 KB: dispatch 78.6 us against 89.1 with ordinary
+// stores, combine 84.8 against 92.8 with ordinary loads).  The gradient of
+// combine keeps ordinary accesses: 170 us against 176 there, but 26.2 against
+// 22.6 for 8000 rows of 8 KB, which the caches hold.
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ uint4 load_once(const uint4* p) {
+  return __builtin_bit_cast(uint4, __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p)));
+}
+__device__ __forceinline__ void store_once(uint4* p, uint4 v) {
+  __builtin_nontemporal_store(__builtin_bit_cast(u32x4, v), reinterpret_cast<u32x4*>(p));
+}
+
 // Block (c, m): pieces 256 c .. of token m's row, to its k sorted rows; and of
 // the sorted rows m k .. m k + k - 1 those that no pair takes, as zeros.
 __global__ __launch_bounds__(kMoveThreads) void moe_dispatch_kernel(MoveArgs a) {
@@ -166,7 +179,7 @@ __global__ __launch_bounds__(kMoveThreads) void moe_dispatch_kernel(MoveArgs a) 
     for (int s = 0; s < a.k; ++s) {
       const long p = m * a.k + s;
       const int r = a.inverse[p];
-      if ((uint32_t)r < (uint32_t)a.P) reinterpret_cast<uint4*>(a.dst)[(size_t)r * a.n16 + c] = v;
+      if ((uint32_t)r < (uint32_t)a.P) store_once(reinterpret_cast<uint4*>(a.dst) + (size_t)r * a.n16 + c, v);
       if (a.order[p] < 0) reinterpret_cast<uint4*>(a.dst)[(size_t)p * a.n16 + c] = make_uint4(0u, 0u, 0u, 0u);
     }
   }
@@ -200,7 +213,10 @@ struct Piece {                                   // 16 bytes of a row as fp32 va
 };
 
 // Block (c, m): pieces 256 c .. of token m: its k sorted rows, weighted, added
-// in fp32 in slot order and rounded once.
+// in fp32 in slot order and rounded once.  The rows of kSlots slots are in
+// flight together; a slot without an expert reads row 0 and leaves it out.
+constexpr int kSlots = 8;
+
 template <bool F32>
 __global__ __launch_bounds__(kMoveThreads) void moe_combine_kernel(MoveArgs a) {
   const int c = (int)blockIdx.x * kMoveThreads + (int)threadIdx.x;
@@ -209,15 +225,23 @@ __global__ __launch_bounds__(kMoveThreads) void moe_combine_kernel(MoveArgs a) {
     Piece<F32> acc;
 #pragma unroll
     for (int i = 0; i < Piece<F32>::N; ++i) acc.v[i] = 0.0f;
-    for (int s = 0; s < a.k; ++s) {
-      const long p = m * a.k + s;
-      const int r = a.inverse[p];
-      if ((uint32_t)r >= (uint32_t)a.P) continue;
-      const float w = a.w ? a.w[p] : 1.0f;
-      Piece<F32> v;
-      v.set(reinterpret_cast<const uint4*>(a.src)[(size_t)r * a.n16 + c]);
+    for (int s0 = 0; s0 < a.k; s0 += kSlots) {
+      int r[kSlots];
+      uint4 raw[kSlots];
 #pragma unroll
-      for (int i = 0; i < Piece<F32>::N; ++i) acc.v[i] = fmaf(w, v.v[i], acc.v[i]);
+      for (int s = 0; s < kSlots; ++s) r[s] = s0 + s < a.k ? a.inverse[m * a.k + s0 + s] : -1;
+#pragma unroll
+      for (int s = 0; s < kSlots; ++s)
+        raw[s] = load_once(reinterpret_cast<const uint4*>(a.src) + (size_t)((uint32_t)r[s] < (uint32_t)a.P ? r[s] : 0) * a.n16 + c);
+#pragma unroll
+      for (int s = 0; s < kSlots; ++s) {
+        if ((uint32_t)r[s] >= (uint32_t)a.P) continue;
+        const float w = a.w ? a.w[m * a.k + s0 + s] : 1.0f;
+        Piece<F32> v;
+        v.set(raw[s]);
+#pragma unroll
+        for (int i = 0; i < Piece<F32>::N; ++i) acc.v[i] = fmaf(w, v.v[i], acc.v[i]);
+      }
     }
     reinterpret_cast<uint4*>(a.dst)[(size_t)m * a.n16 + c] = acc.get();
   }
@@ -247,6 +271,7 @@ __global__ __launch_bounds__(512) void moe_combine_grad_kernel(GradArgs a) {
     if ((uint32_t)r < (uint32_t)a.P) {
       const float w = a.w[p];
       const size_t m = (size_t)(p / a.k);
+#pragma unroll 4
       for (int c = lane; c < a.n16; c += pq::kWave) {
         Piece<F32> g, v;
         g.set(dy[m * a.n16 + c]);
