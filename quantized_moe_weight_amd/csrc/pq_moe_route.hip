@@ -67,31 +67,35 @@ __global__ __launch_bounds__(kSortThreads) void moe_sort_kernel(SortArgs a) {
   __shared__ uint32_t s_total;
   const int tid = (int)threadIdx.x, lane = pq::lane_id(), wv = pq::wave_id();
   const int E = a.E, b = (int)blockIdx.x;
-  for (int i = tid; i < kSortWaves * E; i += kSortThreads) pos[i] = 0;
-  __syncthreads();
-  // counts of each wave's run of pairs
+  // counts of each wave's run of pairs; the ids of its first rounds stay in registers
   const int seg = a.chunk / kSortWaves;
   const long p0 = (long)b * a.chunk + (long)wv * seg;
   uint32_t* mine = pos + wv * E;
-  for (int i = lane; i < seg; i += pq::kWave) {
-    if (p0 + i >= a.P) break;
-    const uint32_t e = (uint32_t)a.ids[p0 + i];
+  auto id_at = [&](int i) { return p0 + i < a.P ? (uint32_t)a.ids[p0 + i] : 0xffffffffu; };
+  constexpr int kKept = kSortChunk / kSortThreads;
+  static_assert(kKept == 2, "two rounds in every chunk");
+  uint32_t kept[kKept];
+#pragma unroll
+  for (int r = 0; r < kKept; ++r) kept[r] = id_at(r * pq::kWave + lane);
+  // thread e: the expert's pairs in all blocks and in the blocks before this one
+  uint32_t total = 0, before = 0;
+  if (tid < E && a.nb > 1) {
+#pragma unroll 8
+    for (int i = 0; i < a.nb; ++i) {
+      const uint32_t c = a.hist[(size_t)i * E + tid];
+      total += c;
+      before += i < b ? c : 0u;
+    }
+  }
+  for (int i = tid; i < kSortWaves * E; i += kSortThreads) pos[i] = 0;
+  __syncthreads();
+  for (int i = 0; i < seg; i += pq::kWave) {
+    const uint32_t e = i < kKept * pq::kWave ? kept[i ? 1 : 0] : id_at(i + lane);
     if (e < (uint32_t)E) atomicAdd(&mine[e], 1u);
   }
   __syncthreads();
-  // thread e: the expert's pairs in all blocks and in the blocks before this one
-  uint32_t total = 0, before = 0;
-  if (tid < E) {
-    if (a.nb > 1) {
-      for (int i = 0; i < a.nb; ++i) {
-        const uint32_t c = a.hist[(size_t)i * E + tid];
-        total += c;
-        before += i < b ? c : 0u;
-      }
-    } else {
-      for (int w = 0; w < kSortWaves; ++w) total += pos[w * E + tid];
-    }
-  }
+  if (tid < E && a.nb == 1)
+    for (int w = 0; w < kSortWaves; ++w) total += pos[w * E + tid];
   // exclusive scan of the totals over the experts
   uint32_t inc = total;
 #pragma unroll
@@ -120,7 +124,7 @@ __global__ __launch_bounds__(kSortThreads) void moe_sort_kernel(SortArgs a) {
   for (int i = 0; i < seg; i += pq::kWave) {               // the whole wave together: seg is a multiple of 64
     const long p = p0 + i + lane;
     const bool in = p < a.P;
-    const uint32_t e = in ? (uint32_t)a.ids[p] : 0xffffffffu;
+    const uint32_t e = i < kKept * pq::kWave ? kept[i ? 1 : 0] : id_at(i + lane);
     const bool has = e < (uint32_t)E;
     const uint64_t m = same_key(has ? e : 0u, a.ebits, __ballot(has));
     const int rank = __popcll(m & ((1ull << lane) - 1ull));
