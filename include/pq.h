@@ -406,9 +406,11 @@ int pq_dequantize_mxfp4(const uint8_t* codes, const uint8_t* scales, int rows, i
  *   y : bf16 [M,N] or [M,N/2] under PQ_EPI_SILU_MUL (gate rows then up rows)
  * Constraints: 1 <= M <= 16, K % 32 == 0, K >= 32, N >= 1, N even under
  * PQ_EPI_SILU_MUL, N*K/2 < 2^31, M*K <= 69632 (the activation lives in one
- * CU's LDS); PQ_ERR_SHAPE otherwise.  An output's bits depend on K, N, the
- * epilogue and the device's CU count, not on M or the other tokens, as long as
- * N is below 2048 rows per CU.  No workspace. */
+ * CU's LDS); PQ_ERR_SHAPE otherwise.  An output's bits do not depend on the
+ * other tokens.  They depend on K, N, the epilogue and the device's CU count,
+ * and on M only where M*K*2 bytes of activation and the partial sums of a CU's
+ * rows pass its LDS together (the rows are then split over more blocks).  No
+ * workspace. */
 int pq_gemv_mxfp4(const uint16_t* x, int M, int K,
                   const uint8_t* w, const uint8_t* w_scale, int N,
                   int epi, uint16_t* y, void* stream);

@@ -412,7 +412,8 @@ class MoeLayerCall:
 # ---------------------------------------------------------------------------
 # MXFP4, and routed rows in expert order.  These calls take their scratch from
 # torch's allocator per call, on the current stream, so calls on several
-# streams and captured graphs never share it.
+# streams and captured graphs never share it.  They record no autograd graph:
+# the gradients are calls of their own.
 # ---------------------------------------------------------------------------
 
 _current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
@@ -672,7 +673,12 @@ def moe_prefill_layer_mxfp4(x, w13, s13, w2, s2, topk_ids, topk_w, out=None):
     x bf16 [M,H]; w13 codes [E,2I,H/2], s13 bytes [E,2I,H/32] (gate rows, then up rows); w2 codes [E,H,I/2], s2 bytes
     [E,H,I/32]; topk_ids int32 [M,top_k] (outside [0,E): no expert), topk_w fp32 [M,top_k].  Both products quantise
     their input live, as moe_decode_layer does.  Returns y bf16 [M,H]."""
+    _need_here(x, _BF16, 2, "x")
     _need_here(w13, _U8, 3, "w13")
+    _need_here(w2, _U8, 3, "w2")
+    H, I = x.shape[1], w2.shape[2] * 2
+    if tuple(w13.shape[1:]) != (2 * I, H // 2) or tuple(w2.shape[:2]) != (w13.shape[0], H):
+        raise ValueError("w13 must be [E, 2I, H/2] and w2 [E, H, I/2] for x [M, H]")
     plan = moe_sort(topk_ids, w13.shape[0])
     h = gemm_mxfp4_grouped(x, w13, s13, plan, EPI_SILU_MUL)
     return moe_combine(gemm_mxfp4_grouped(h, w2, s2, plan, gather=False), plan, topk_w, out)

@@ -113,15 +113,14 @@ __device__ __forceinline__ void tile_starts(const GArgs& a, int* start) {
   __syncthreads();
 }
 
-// The expert whose row tiles hold row tile mt.
+// The expert whose row tiles hold row tile mt: the last e with start[e] <= mt,
+// found by the whole wave in two reads.
 __device__ __forceinline__ int expert_of(const GArgs& a, const int* start, int mt) {
-  int lo = 0, hi = a.E;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if (start[mid] <= mt) lo = mid;
-    else hi = mid;
-  }
-  return lo;
+  static_assert(kMaxExperts <= 16 * pq::kWave, "two levels of 64 and 16");
+  const int lane = pq::lane_id();
+  const int hi = __popcll(__ballot(start[min(16 * lane, a.E)] <= mt)) - 1;
+  const int lo = __popcll(__ballot(lane < 16 && start[min(16 * hi + lane, a.E)] <= mt)) - 1;
+  return 16 * hi + lo;
 }
 
 // x row of row r (of n_rows) of the expert whose rows start at `first`; -1 past them
@@ -149,10 +148,13 @@ __device__ __forceinline__ int b_row(const GArgs& a, int tile_n, int r) {
 // rows behind the last expert's: zeros
 __device__ __forceinline__ void zero_tail(const GArgs& a, int threads) {
   if (!a.offsets) return;
-  const int end = min(max(a.offsets[a.E], 0), a.P);
-  for (long i = (long)end * a.R + (long)blockIdx.x * threads + threadIdx.x; i < (long)a.P * a.R;
-       i += (long)gridDim.x * threads)
-    a.y[i] = 0;
+  const long from = (long)min(max(a.offsets[a.E], 0), a.P) * a.R, to = (long)a.P * a.R;
+  const long at = (long)blockIdx.x * threads + threadIdx.x, by = (long)gridDim.x * threads;
+  if (a.R % 8 == 0) {
+    for (long i = from / 8 + at; i < to / 8; i += by) reinterpret_cast<uint4*>(a.y)[i] = make_uint4(0u, 0u, 0u, 0u);
+  } else {
+    for (long i = from + at; i < to; i += by) a.y[i] = 0;
+  }
 }
 
 // ---------------------------------------------------------------------------

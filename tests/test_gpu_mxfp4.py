@@ -243,12 +243,31 @@ def test_gemm_tiles_agree(pq, monkeypatch, M, K, N, silu):
 def test_gemm_nan_rows_stay_alone(pq):
     import torch
     rng = np.random.default_rng(8)
-    x, xv = _bf16(rng.standard_normal((40, 160)))
-    w, s, wv = _weights(rng, 70, 160)
-    x[7, 5] = float("inf")
-    y = pq.gemm_mxfp4(x, w, s)
-    assert torch.isnan(y[7]).all()
-    assert torch.isfinite(y[torch.arange(40, device="cuda") != 7]).all()
+    for K in (160, 256, 1152):                                     # both kernels, last scales part of a load
+        x, xv = _bf16(rng.standard_normal((140, K)))
+        w, s, wv = _weights(rng, 70, K)
+        x[7, K - 1] = float("inf")
+        x[139, 0] = float("nan")
+        y = pq.gemm_mxfp4(x, w, s)
+        assert torch.isnan(y[[7, 139]]).all()
+        row = torch.arange(140, device="cuda")
+        assert torch.isfinite(y[(row != 7) & (row != 139)]).all()
+
+
+def test_gemv_activation_and_sums_past_one_cus_lds(pq):
+    """139 KB of activation leave room for few partial sums: the rows are split over more blocks than CUs."""
+    rng = np.random.default_rng(12)
+    for M, K, N, silu in ((16, 4352, 20002, True), (2, 34816, 60000, False)):
+        x, xv = _bf16(rng.standard_normal((M, K)))
+        p = rng.integers(0, 256, (N, K // 2), dtype=np.uint8)
+        b = rng.integers(118, 123, (N, K // 32), dtype=np.uint8)
+        y = pq.gemv_mxfp4(x, _t(p), _t(b), pq.EPI_SILU_MUL if silu else pq.EPI_NONE)
+        R = N // 2 if silu else N
+        at = np.unique(np.concatenate([rng.integers(0, R, 300), [0, 1, R - 2, R - 1]]))
+        rows = np.concatenate([at, at + R]) if silu else at
+        want, bound = expect(xv, oracle.mx_values(p[rows], b[rows]), silu)
+        import torch
+        close(y[:, torch.from_numpy(at).cuda()], want, bound, f"M={M} K={K} N={N}")
 
 
 def _routing(rng, M, k, E, how):
@@ -419,6 +438,15 @@ def test_refusals(pq, monkeypatch):
         pq.dequantize_mxfp4(w, s, torch.float16)
     with pytest.raises(ValueError):
         pq.dequantize_mxfp4(w, s[:, :1].contiguous())
+    e4 = torch.zeros((4, 2), dtype=torch.int32, device="cuda")
+    tw = torch.ones((4, 2), device="cuda")
+    w13, s13 = torch.zeros((3, 64, 32), dtype=torch.uint8, device="cuda"), torch.zeros((3, 64, 2), dtype=torch.uint8, device="cuda")
+    w2, s2 = torch.zeros((3, 64, 16), dtype=torch.uint8, device="cuda"), torch.zeros((3, 64, 1), dtype=torch.uint8, device="cuda")
+    assert tuple(pq.moe_prefill_layer_mxfp4(x, w13, s13, w2, s2, e4, tw).shape) == (4, 64)
+    for bad in ((w13[:2].contiguous(), s13[:2].contiguous(), w2, s2), (w13, s13, w2[:, :32].contiguous(), s2[:, :32].contiguous()),
+                (w13[:, :32].contiguous(), s13[:, :32].contiguous(), w2, s2)):
+        with pytest.raises(ValueError):
+            pq.moe_prefill_layer_mxfp4(x, *bad, e4, tw)
     buf = torch.zeros(64 * 64, dtype=torch.bfloat16, device="cuda")
     with pytest.raises(ValueError):                 # an output on top of an input that other blocks still read
         pq.gemv_mxfp4(buf[:256].view(4, 64), w, s, out=buf[128:160].view(4, 8))
