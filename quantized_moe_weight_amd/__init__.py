@@ -493,9 +493,10 @@ def dequantize_mxfp4(codes, scales, dtype=torch.bfloat16, out=None):
 def _mx_weights(w, w_scale, K, ndim):
     _need_here(w, _U8, ndim, "w")
     _need_here(w_scale, _U8, ndim, "w_scale")
-    if w.shape[-1] * 2 != K or w_scale.shape[:-1] != w.shape[:-1] or w_scale.shape[-1] * 32 != K:
+    ws, ss = w.shape, w_scale.shape
+    if ws[-1] * 2 != K or ss[-1] * 32 != K or ws[-2] != ss[-2] or ws[0] != ss[0]:
         raise ValueError("weight / scale shapes do not match x")
-    return w.shape[-2]
+    return ws[-2]
 
 
 def gemv_mxfp4(x, w, w_scale, epi: int = EPI_NONE, out=None):
@@ -565,7 +566,9 @@ def moe_sort(topk_ids, E: int) -> MoePlan:
     An id outside [0, E) stands for no expert (a padded token)."""
     _need_here(topk_ids, _I32, 2, "topk_ids")
     M, k = topk_ids.shape
-    plan = MoePlan(topk_ids.new_empty(M * k), topk_ids.new_empty((M, k)), topk_ids.new_empty(max(int(E), 0) + 1))
+    if not 1 <= E <= 1024:
+        raise PqError("pq_moe_sort", -2)
+    plan = MoePlan(topk_ids.new_empty(M * k), topk_ids.new_empty((M, k)), topk_ids.new_empty(E + 1))
     wsn = int(_lib.load().pq_moe_sort_workspace(M, k, E))
     ws = topk_ids.new_empty(wsn, dtype=torch.uint8) if wsn else None
     _check(_lib.load().pq_moe_sort(_a(topk_ids), M, k, E, _a(plan.order), _a(plan.inverse), _a(plan.offsets), _a(ws), wsn,
@@ -679,6 +682,7 @@ def moe_prefill_layer_mxfp4(x, w13, s13, w2, s2, topk_ids, topk_w, out=None):
     H, I = x.shape[1], w2.shape[2] * 2
     if tuple(w13.shape[1:]) != (2 * I, H // 2) or tuple(w2.shape[:2]) != (w13.shape[0], H):
         raise ValueError("w13 must be [E, 2I, H/2] and w2 [E, H, I/2] for x [M, H]")
+    _need_here(topk_w, _F32, 2, "topk_w")
     plan = moe_sort(topk_ids, w13.shape[0])
     h = gemm_mxfp4_grouped(x, w13, s13, plan, EPI_SILU_MUL)
     return moe_combine(gemm_mxfp4_grouped(h, w2, s2, plan, gather=False), plan, topk_w, out)

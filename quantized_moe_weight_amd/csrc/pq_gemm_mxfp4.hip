@@ -266,10 +266,9 @@ __global__ __launch_bounds__(kThreads) void gemm_mxfp4_tiled_kernel(GArgs a) {
     soff = r >= 0 ? (uint32_t)r * nb : pq::kOOB;
   };
 
-  // the loads of step k into stage s (zeros past the last step, so that every
-  // step issues the same number); a last step of 4 blocks has no upper half
+  // the codes of step k into stage s; a last step of 4 blocks has no upper half
   auto issue = [&](int s, int k) {
-    const bool ok = k < nk && (8 * k + 8 <= nb || piece < 4);
+    const bool ok = 8 * k + 8 <= nb || piece < 4;
     const uint32_t kofs = (uint32_t)__builtin_amdgcn_readfirstlane(k * kRowBytes);
 #pragma unroll
     for (int i = 0; i < LA; ++i)
@@ -370,10 +369,10 @@ __global__ __launch_bounds__(kThreads) void gemm_mxfp4_tiled_kernel(GArgs a) {
     }
 
     // Results.  Lane (g, c) of sub-tile (i, j) holds row c of i, columns 4g ..
-    // 4g+3 of j: 32 bytes of a row per store instruction.  So up to 4 KB at a time go
-    // through the wave's part of the last stage (not loaded again before the
-    // next barrier) and out as lines; its 16-byte slots are swizzled by row
-    // like the operands'.
+    // 4g+3 of j: 32 bytes of a row per store instruction.  So up to 4 KB at a
+    // time go through the wave's part of the last stage (not loaded again
+    // before the next barrier) and out as lines; its 16-byte slots are swizzled
+    // by row like the operands'.
     constexpr int CW = SILU ? CN / 2 : CN;                   // 16-column sub-tiles of results
     constexpr int ROWB = 32 * CW, SLOTS = 2 * CW;            // bytes and slots of a row of the box
     constexpr int RI = WM < BN / ROWB ? WM : BN / ROWB;      // row sub-tiles in the box
@@ -406,15 +405,15 @@ __global__ __launch_bounds__(kThreads) void gemm_mxfp4_tiled_kernel(GArgs a) {
       for (int q = 0; q < 16 * RI / PER; ++q) {
         const int r = PER * q + lane / SLOTS;
         const uint4 v = *reinterpret_cast<const uint4*>(box + ROWB * r + 16 * ((lane % SLOTS) ^ swz(r)));
-        const int down = (16 * i0 + PER * q) * a.R * 2;
+        const uint32_t at = to + (uint32_t)((16 * i0 + PER * q) * a.R) * 2u;
         if (a.R % 8 == 0) {
-          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(int32x4u, v), yr, (int)to, down, 0);
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(int32x4u, v), yr, (int)at, 0, 0);
         } else {
           const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
           for (int c = 0; c < 8; ++c)
             if (col + c < a.R)
-              __builtin_amdgcn_raw_buffer_store_b16((short)(uint16_t)(w[c >> 1] >> (16 * (c & 1))), yr, (int)(to + 2 * c), down, 0);
+              __builtin_amdgcn_raw_buffer_store_b16((short)(uint16_t)(w[c >> 1] >> (16 * (c & 1))), yr, (int)(at + 2 * c), 0, 0);
         }
       }
       asm volatile("" ::: "memory");

@@ -172,7 +172,7 @@ def test_refusals(pq, monkeypatch):
         pq.moe_sort(ids.long(), 4)
     with pytest.raises(ValueError):
         pq.moe_sort(ids[:, :1], 4)
-    for bad in (0, 1025, -3):
+    for bad in (0, 1025, -3, 2 ** 32 + 4):
         with pytest.raises(pq.PqError):
             pq.moe_sort(ids, bad)
     with pytest.raises(pq.PqError):

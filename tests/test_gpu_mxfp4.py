@@ -315,11 +315,12 @@ def test_grouped(pq, M, k, E, K, N, silu, how):
         assert torch.equal(pq.gemm_mxfp4_grouped_prequant(xq, xs, w, s, plan, epi, gather=gather), y)
 
 
-def test_grouped_offsets_out_of_range_stay_inside(pq):
+@pytest.mark.parametrize("K", [64, 128])
+def test_grouped_offsets_out_of_range_stay_inside(pq, K):
     """Offsets and order entries that moe_sort does not make are clamped: no access leaves x, w or y."""
     import torch
     rng = np.random.default_rng(0)
-    M, k, E, K, N = 8, 2, 4, 64, 32
+    M, k, E, N = 8, 2, 4, 32
     w, s, _ = _weights(rng, E, N, K)
     x, _ = _bf16(rng.standard_normal((M, K)))
     guard = torch.zeros((3 * M * k, N), dtype=torch.bfloat16, device="cuda")
@@ -447,6 +448,8 @@ def test_refusals(pq, monkeypatch):
                 (w13[:, :32].contiguous(), s13[:, :32].contiguous(), w2, s2)):
         with pytest.raises(ValueError):
             pq.moe_prefill_layer_mxfp4(x, *bad, e4, tw)
+    with pytest.raises(TypeError):
+        pq.moe_prefill_layer_mxfp4(x, w13, s13, w2, s2, e4, None)
     buf = torch.zeros(64 * 64, dtype=torch.bfloat16, device="cuda")
     with pytest.raises(ValueError):                 # an output on top of an input that other blocks still read
         pq.gemv_mxfp4(buf[:256].view(4, 64), w, s, out=buf[128:160].view(4, 8))
@@ -456,6 +459,8 @@ def test_refusals(pq, monkeypatch):
         pq.gemm_mxfp4_grouped(x, wg[:2].contiguous(), sg[:2].contiguous(), plan)
     with pytest.raises(ValueError):
         pq.gemm_mxfp4_grouped(x, wg, sg, plan, gather=False)
+    with pytest.raises(ValueError):
+        pq.gemm_mxfp4_grouped(x, wg, sg[:, :4].contiguous(), plan)
     monkeypatch.setattr(pq, "_current_device", lambda: 1)
     with pytest.raises(ValueError):                 # a tensor of another device than the current one
         pq.gemv_mxfp4(x, w, s)
