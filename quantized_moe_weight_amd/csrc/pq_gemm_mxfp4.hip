@@ -383,7 +383,7 @@ __global__ __launch_bounds__(kThreads) void gemm_mxfp4_tiled_kernel(GArgs a) {
                                         (uint32_t)min(left, BM / 2) * (uint32_t)a.R * 2u);
     uint8_t* box = st.b[S - 1] + wv * (BN * kRowBytes / (kThreads / pq::kWave));
     const int col = d.tile_n * (SILU ? BN / 2 : BN) + 16 * CW * wn + 8 * (lane % SLOTS);
-    const uint32_t to = col < a.R ? (uint32_t)(lane / SLOTS) * (uint32_t)a.R * 2u + 2u * (uint32_t)col : pq::kOOB;
+    uint32_t to = col < a.R ? (uint32_t)(lane / SLOTS) * (uint32_t)a.R * 2u + 2u * (uint32_t)col : pq::kOOB;
     auto swz = [](int r) { return r / (8 / SLOTS) % SLOTS; };
 #pragma unroll
     for (int i0 = 0; i0 < WM; i0 += RI) {
@@ -405,16 +405,16 @@ __global__ __launch_bounds__(kThreads) void gemm_mxfp4_tiled_kernel(GArgs a) {
       for (int q = 0; q < 16 * RI / PER; ++q) {
         const int r = PER * q + lane / SLOTS;
         const uint4 v = *reinterpret_cast<const uint4*>(box + ROWB * r + 16 * ((lane % SLOTS) ^ swz(r)));
-        const uint32_t at = to + (uint32_t)((16 * i0 + PER * q) * a.R) * 2u;
         if (a.R % 8 == 0) {
-          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(int32x4u, v), yr, (int)at, 0, 0);
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(int32x4u, v), yr, (int)to, 0, 0);
         } else {
           const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
           for (int c = 0; c < 8; ++c)
             if (col + c < a.R)
-              __builtin_amdgcn_raw_buffer_store_b16((short)(uint16_t)(w[c >> 1] >> (16 * (c & 1))), yr, (int)(at + 2 * c), 0, 0);
+              __builtin_amdgcn_raw_buffer_store_b16((short)(uint16_t)(w[c >> 1] >> (16 * (c & 1))), yr, (int)(to + 2 * c), 0, 0);
         }
+        to += (uint32_t)PER * (uint32_t)a.R * 2u;
       }
       asm volatile("" ::: "memory");
     }
