@@ -405,6 +405,95 @@ def test_prefill_layer_in_a_graph_and_on_another_stream(pq):
             assert torch.equal(o, want[rep % 3]) and torch.equal(eager, want[rep % 3])
 
 
+def test_single_calls_in_a_graph(pq):
+    """Each call captured with others on one stream; every replay equals the eager calls on the same buffers."""
+    import torch
+    rng = np.random.default_rng(21)
+    M, k, E, H = 300, 8, 16, 512
+    w, s, _ = _weights(rng, 96, H)
+    sets = []
+    for _ in range(3):
+        x, _ = _bf16(rng.standard_normal((M, H)))
+        dy, _ = _bf16(rng.standard_normal((M, H)))
+        sets.append((x, dy, _t(_routing(rng, M, k, E, "drop")), _t(rng.random((M, k)).astype(np.float32))))
+    bufs = [t.clone() for t in sets[0]]
+
+    def calls(x, dy, ids, tw):
+        few = x[:12].contiguous()
+        plan = pq.moe_sort(ids, E)
+        xs = pq.moe_dispatch(x, plan)
+        return [pq.gemv_mxfp4(few, w, s), pq.gemv_mxfp4(few, w, s, pq.EPI_SILU_MUL), pq.gemm_mxfp4(x, w, s),
+                pq.dequantize_mxfp4(*pq.quantize_mxfp4(x)), *plan, xs, pq.moe_combine(xs, plan, tw),
+                pq.moe_dispatch_grad(xs, plan), *pq.moe_combine_grad(dy, xs, plan, tw)]
+
+    want = [calls(*c) for c in sets]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = calls(*bufs)
+    for rep in range(5):
+        for b, t in zip(bufs, sets[rep % 3]):
+            b.copy_(t)
+        g.replay()
+        eager = calls(*bufs)
+        torch.cuda.synchronize()
+        for a, b, c in zip(got, eager, want[rep % 3]):
+            assert torch.equal(a, c) and torch.equal(b, c)
+
+
+def test_two_threads_on_two_streams(pq):
+    """Calls of two host threads at once, each on its own stream, share nothing."""
+    import threading
+    import torch
+    rng = np.random.default_rng(31)
+    M, k, E, H, I = 200, 4, 8, 256, 128
+    w13, s13, _ = _weights(rng, E, 2 * I, H)
+    w2, s2, _ = _weights(rng, E, H, I)
+    jobs = []
+    for _ in range(2):
+        x, _ = _bf16(rng.standard_normal((M, H)))
+        a = (x, w13, s13, w2, s2, _t(_routing(rng, M, k, E, "drop")), _t(rng.random((M, k)).astype(np.float32)))
+        jobs.append((a, pq.moe_prefill_layer_mxfp4(*a)))
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(a, want):
+        st = torch.cuda.Stream()
+        with torch.cuda.stream(st):
+            outs = [pq.moe_prefill_layer_mxfp4(*a) for _ in range(20)]
+        st.synchronize()
+        bad.extend(o for o in outs if not torch.equal(o, want))
+
+    threads = [threading.Thread(target=work, args=j) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
+
+
+def test_past_4_gib(pq):
+    """Byte offsets past 32 bits: in the quantiser's input, and in the grouped product's rows."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn((70000, 32768), generator=g, device="cuda", dtype=torch.bfloat16)      # 4.6 GB
+    codes, scales = pq.quantize_mxfp4(x)
+    c, s = pq.quantize_mxfp4(x[-300:].contiguous())
+    assert torch.equal(codes[-300:], c) and torch.equal(scales[-300:], s)
+    assert torch.equal(pq.dequantize_mxfp4(codes, scales)[-300:], pq.dequantize_mxfp4(c, s))
+    del x, codes, scales
+    M, k, E, K, N = 100000, 2, 4, 128, 12288                                                # 4.9 GB of results
+    ids = torch.randint(0, E, (M, k), generator=g, device="cuda", dtype=torch.int32)
+    x = torch.randn((M, K), generator=g, device="cuda", dtype=torch.bfloat16)
+    w = torch.randint(0, 256, (E, N, K // 2), generator=g, device="cuda", dtype=torch.uint8)
+    ws = torch.randint(118, 123, (E, N, K // 32), generator=g, device="cuda", dtype=torch.uint8)
+    plan = pq.moe_sort(ids, E)
+    y = pq.gemm_mxfp4_grouped(x, w, ws, plan)
+    last = pq.moe_dispatch(x, plan)[-500:].contiguous()
+    assert torch.equal(y[-500:], pq.gemm_mxfp4(last, w[E - 1], ws[E - 1]))
+    first = pq.moe_dispatch(x, plan)[:500].contiguous()
+    assert torch.equal(y[:500], pq.gemm_mxfp4(first, w[0], ws[0]))
+
+
 # ---------------------------------------------------------------------------
 # refusals of the binding
 # ---------------------------------------------------------------------------
